@@ -427,6 +427,156 @@ SPIN_API spin_status spin_state_qquant(spin_state st, const uint8_t** q8, const 
 SPIN_API int64_t spin_score_stride(spin_state st);
 SPIN_API int64_t spin_mask_stride(spin_state st);
 
+/* ---------------------------------------------------------------------------
+ * Core attention around the indexer: rotary positions, the paged latent cache
+ * and the attention that reads it.
+ *
+ * The token top-k above is the input of a sparse attention layer (SPIN
+ * digest, arXiv深度剖析: the selected tokens go to core attention).  These calls
+ * are that layer's operators, with keys and values from one shared latent
+ * vector a token.  A token's cache entry is [c | kr]: the latent c
+ * (latent_dim) and one rotated key part kr (rope_dim) that all heads share.
+ * Two equal forms of the attention exist, for heads h with projections
+ * k = [W_uk c | kr], v = W_uv c:
+ *   absorbed (decode): the query is taken into the latent space beforehand,
+ *     q_latent = W_uk^T q_nope, so a head attends to the entries themselves:
+ *       s_j = scale * (q_latent . c_j + q_rope . kr_j),  p = softmax(s),
+ *       out = sum_j p_j c_j      (the caller applies W_uv afterwards);
+ *   expanded (a chunk of new tokens): k_j and v_j are formed once for the
+ *     whole context, out = sum_j p_j v_j with s_j = scale * q . k_j.
+ * Positions are those of the decode step above: row r of request q sits at
+ * p_r = ctx_len[q] - 1 + r and sees slots 0..p_r; a position is a slot index.
+ * The conventions at the top of this file hold: asynchronous, no allocation,
+ * argument errors in the return value, device-side errors in the handle's own
+ * device error word (spin_latent_error), deterministic results. */
+typedef enum {
+  SPIN_ROPE_INTERLEAVED = 0, /* element pairs (2 i, 2 i + 1) */
+  SPIN_ROPE_HALF = 1         /* element pairs (i, i + rope_dim / 2) */
+} spin_rope_layout;
+
+/* Pair i turns by position * f_i, with f_i = base^(-2 i / rope_dim) and
+ *   SPIN_ROPE_PLAIN   nothing else;
+ *   SPIN_ROPE_LINEAR  f_i / factor (position interpolation);
+ *   SPIN_ROPE_YARN    (1 - g_i) f_i + g_i f_i / factor, where g_i rises from 0
+ *     to 1 between the pairs that turn beta_fast and beta_slow times within
+ *     rope_original positions (YaRN, arXiv 2309.00071), cos and sin
+ *     multiplied by attn_factor (0: the method's 0.1 ln(factor) + 1). */
+typedef enum { SPIN_ROPE_PLAIN = 0, SPIN_ROPE_LINEAR = 1, SPIN_ROPE_YARN = 2 } spin_rope_scaling;
+
+typedef struct {
+  int32_t num_requests;   /* Q: request slots */
+  int32_t max_slots;      /* KV capacity per request (slots) */
+  int32_t block_size;     /* b: tokens per page, a power of two in 16..256 */
+  int32_t num_heads;      /* attention heads, 1..256 */
+  int32_t latent_dim;     /* width of c: a multiple of 8 in 8..512 */
+  int32_t rope_dim;       /* width of kr and of every rotation: a multiple of 8 in 8..128 */
+  int32_t nope_dim;       /* expanded form: key width without kr, a multiple of 8 in 8..256 */
+  int32_t v_dim;          /* expanded form: value width, a multiple of 8 in 8..256 */
+  int32_t topk;           /* entries of a top-k list, 1..65536 */
+  int32_t max_rows;       /* 1..4 query rows of spin_latent_attention */
+  int32_t prefill_slots;  /* expanded form: slots that one call can expand, over all requests, each request
+                             rounded up to 128; a multiple of 128, or 0 without spin_latent_prefill
+                             (nope_dim and v_dim are then not looked at) */
+  int32_t dtype;          /* SPIN_BF16 or SPIN_F32: cache, queries, weights and outputs */
+  int32_t rope_layout;    /* spin_rope_layout */
+  int32_t rope_scaling;   /* spin_rope_scaling */
+  int32_t rope_original;  /* SPIN_ROPE_YARN: positions the frequencies were made for, >= 1 */
+  float softmax_scale;    /* scale of the logits, finite and > 0 */
+  float beta_fast;        /* SPIN_ROPE_YARN (32), > beta_slow */
+  float beta_slow;        /* SPIN_ROPE_YARN (1), > 0 */
+  float attn_factor;      /* SPIN_ROPE_YARN: factor on cos and sin, or 0 */
+  int32_t reserved;       /* 0 */
+  double rope_base;       /* > 1 */
+  double rope_factor;     /* SPIN_ROPE_LINEAR and _YARN, >= 1 */
+} spin_latent_config;
+
+typedef struct spin_latent_s* spin_latent;
+
+/* Bytes of device memory a handle needs: the error word, the partial sums of
+ * a context that several thread blocks share, and for prefill_slots > 0 the
+ * expanded keys and values (prefill_slots * (num_heads * (nope_dim + v_dim) +
+ * rope_dim) elements).  Returns 0 for an invalid config. */
+SPIN_API size_t spin_latent_bytes(const spin_latent_config* cfg);
+
+/* Creates a handle over the caller's device block dev_mem (>=
+ * spin_latent_bytes, 256-byte aligned, alive until spin_latent_destroy).  The
+ * handle belongs to the device that holds dev_mem: every call runs there,
+ * whatever device is current, and its stream must be one of that device.
+ * Calls on one handle share its scratch: use it from one stream at a time,
+ * and do not let two CUDA graphs captured from it run at once. */
+SPIN_API spin_status spin_latent_create(const spin_latent_config* cfg, void* dev_mem, size_t bytes,
+                                        spin_stream_t stream, spin_latent* out);
+SPIN_API spin_status spin_latent_destroy(spin_latent lt);
+
+/* Rotates elements [offset, offset + rope_dim) of each head and copies the
+ * others: x, out [tokens][heads][head_dim] in the handle's dtype, with element
+ * strides between tokens and between heads (the head itself is contiguous).
+ * positions_dev [tokens] int32, of either sign: -p undoes p (a rotation's
+ * transpose), up to attn_factor.  out == x with x's strides rotates in
+ * place; any other overlap is not allowed.  Angles are exact to 2^-31 of a
+ * turn at every position: the turn's fraction is an integer product modulo
+ * 2^64. */
+SPIN_API spin_status spin_rope(spin_latent lt, int64_t tokens, int heads, int head_dim, int offset, const void* x,
+                               int64_t x_token_stride, int64_t x_head_stride, const int32_t* positions_dev,
+                               void* out, int64_t out_token_stride, int64_t out_head_stride, spin_stream_t stream);
+
+/* Writes new tokens into the cache [num_pages][b][latent_dim + rope_dim]: for
+ * r < row_count_dev[q] (NULL: rows) slot p_r of request q becomes
+ * [c | kr rotated by p_r].  c_dev and kr_dev hold token (q, r) at
+ * (q * rows + r) times their token stride (elements).  Other cache entries
+ * stay as they are.  block_table [Q][bt_stride] as for the indexer.  A
+ * request with ctx_len < 1, a row_count outside 0..rows or a last slot past
+ * max_slots sets ERR_CTX_LEN (bit 0) or ERR_ACCEPTED (bit 2) and writes
+ * nothing; a page outside the cache sets ERR_PAGE (bit 1) and that token is
+ * not written.  Two rows that share a slot of one page leave either's entry. */
+SPIN_API spin_status spin_latent_append(spin_latent lt, int rows, const void* c_dev, int64_t c_token_stride,
+                                        const void* kr_dev, int64_t kr_token_stride, void* cache, int32_t num_pages,
+                                        const int32_t* block_table, int32_t bt_stride, const int32_t* ctx_len_dev,
+                                        const int32_t* row_count_dev, spin_stream_t stream);
+
+/* Absorbed attention of 1..max_rows query rows per request.
+ *   q_latent [Q][rows][num_heads][latent_dim] and q_rope [..][rope_dim]
+ *   (rotated), each with its element strides between tokens (q, r) and heads;
+ *   topk_dev [Q][rows][topk] int32 as spin_topk writes it: row r attends to
+ *   the entries in 0..p_r, in any order and each as often as it is listed;
+ *   others (the -1 padding) are skipped.  NULL: row r attends to all of
+ *   0..p_r;
+ *   out [Q][rows][num_heads][latent_dim] in dtype, lse [Q][rows][num_heads]
+ *   fp32 (NULL: not written): the natural logarithm of the sum of exp(s_j).
+ * A row that attends to nothing gets out = 0 and lse = -inf, as does a
+ * request whose ctx_len is out of range (ERR_CTX_LEN).  A slot whose page
+ * lies outside the cache sets ERR_PAGE and is skipped.  Entries that a row
+ * does not attend to never reach it, whatever they hold. */
+SPIN_API spin_status spin_latent_attention(spin_latent lt, int rows, const void* cache, int32_t num_pages,
+                                           const int32_t* block_table, int32_t bt_stride, const void* q_latent,
+                                           int64_t ql_token_stride, int64_t ql_head_stride, const void* q_rope,
+                                           int64_t qr_token_stride, int64_t qr_head_stride,
+                                           const int32_t* ctx_len_dev, const int32_t* topk_dev, void* out,
+                                           float* lse, spin_stream_t stream);
+
+/* Expanded attention of a chunk of new tokens over the paged context that
+ * holds them already (spin_latent_append).  Rows r < row_count_dev[q] (NULL:
+ * rows) of request q attend to slots 0..p_r.
+ *   q [Q][rows][num_heads][nope_dim + rope_dim], the last rope_dim elements
+ *   rotated, with element strides between tokens and heads;
+ *   w_kv [num_heads][nope_dim + v_dim][latent_dim] contiguous: W_uk then W_uv
+ *   of each head;
+ *   out [Q][rows][num_heads][v_dim]; rows >= row_count are left as they are.
+ * Expanded keys and values are rounded to dtype.  A request whose lengths are
+ * out of range sets ERR_CTX_LEN or ERR_ACCEPTED, one that no longer fits
+ * prefill_slots (in request order) ERR_CAPACITY (bit 4), one with a page
+ * outside the cache among those of its slots ERR_PAGE; its rows stay
+ * unwritten.  Slots past a request's last row never reach the result. */
+SPIN_API spin_status spin_latent_prefill(spin_latent lt, int rows, const void* cache, int32_t num_pages,
+                                         const int32_t* block_table, int32_t bt_stride, const void* q,
+                                         int64_t q_token_stride, int64_t q_head_stride, const void* w_kv,
+                                         const int32_t* ctx_len_dev, const int32_t* row_count_dev, void* out,
+                                         spin_stream_t stream);
+
+/* Synchronises `stream`, then reads and clears the handle's device error
+ * word, as spin_get_error does for a state. */
+SPIN_API spin_status spin_latent_error(spin_latent lt, spin_stream_t stream, uint32_t* word_out);
+
 #ifdef __cplusplus
 }
 #endif

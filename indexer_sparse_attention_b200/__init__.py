@@ -123,6 +123,7 @@ def load():
         "spin_score_stride": (_i64, [_vp]),
         "spin_mask_stride": (_i64, [_vp]),
     }
+    sig.update(latent.SIGNATURES)
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
         fn.restype = res
@@ -430,3 +431,10 @@ def spin_state_import(st: SpinState, blob: bytes, stream=None) -> None:
 
 def spin_status_string(status: int) -> str:
     return load().spin_status_string(status).decode()
+
+
+# the core-attention entry points (rotary positions, latent cache and attention)
+from . import latent  # noqa: E402
+from .latent import *  # noqa: E402,F401,F403
+
+__all__ += latent.__all__

@@ -1,0 +1,387 @@
+// k_latent_simt.cu -- absorbed and expanded latent attention on the CUDA
+// cores: every dtype, width and alignment, and the join of shared items.
+//
+// One pass over the tokens with a running maximum m and sum l per head:
+//   m' = max(m, s_j),  l' = l 2^(m - m') + sum 2^(s_j - m'),
+//   o' = o 2^(m - m') + sum 2^(s_j - m') v_j
+// in log2 units (the softmax scale carries log2 e), everything in fp32.
+#include "latent_internal.cuh"
+
+namespace spin {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kNH = kSimtHeads, kT = kSimtTile;
+constexpr float kNegInf = -INFINITY;
+
+// The running softmax of kNH query vectors over tiles of kT tokens.  Warp h
+// owns vector h's statistics; thread i the output columns i and i + 256.
+// kv rows in shared memory have an odd stride, so a column read across tokens
+// has no bank conflicts.
+struct Tile {
+  float* q;     // [kNH][W]
+  float* kv;    // [kT][stride]
+  float* p;     // [kNH][kT]
+  float* alpha; // [kNH]
+  int W, stride, voff, dv;
+
+  // Scores of this thread's (vector warp, token lane), the running softmax
+  // and the output update.  `seen`: whether this vector attends to this token.
+  __device__ __forceinline__ void step(float& m, float& l, float (&o)[2][kNH], float scale, bool seen) const {
+    const int h = threadIdx.x >> 5, j = threadIdx.x & 31;
+    const float* qh = q + h * W;
+    const float* kj = kv + j * stride;
+    float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
+    for (int i = 0; i < W; i += 4) {  // W is a multiple of 8
+      s0 = fmaf(qh[i], kj[i], s0);
+      s1 = fmaf(qh[i + 1], kj[i + 1], s1);
+      s2 = fmaf(qh[i + 2], kj[i + 2], s2);
+      s3 = fmaf(qh[i + 3], kj[i + 3], s3);
+    }
+    const float s = seen ? ((s0 + s1) + (s2 + s3)) * scale : kNegInf;
+    float mt = s;
+#pragma unroll
+    for (int d = 16; d >= 1; d >>= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, d));
+    const float mn = fmaxf(m, mt);
+    const float ref = mn == kNegInf ? 0.f : mn;  // nothing seen yet: every weight 0
+    const float e = seen ? exp2f(s - ref) : 0.f;
+    const float al = exp2f(m - ref);
+    float sum = e;
+#pragma unroll
+    for (int d = 16; d >= 1; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+    l = l * al + sum;
+    m = mn;
+    p[h * kT + j] = e;
+    if (j == 0) alpha[h] = al;
+    __syncthreads();
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const int d = threadIdx.x + c * kThreads;
+      if (d >= dv) continue;
+#pragma unroll
+      for (int h2 = 0; h2 < kNH; ++h2) o[c][h2] *= alpha[h2];
+      const float* v = kv + voff + d;
+      for (int t = 0; t < kT; ++t) {
+        const float x = v[t * stride];
+#pragma unroll
+        for (int h2 = 0; h2 < kNH; ++h2) {
+          // a weight of exactly 0 takes nothing from the token, whatever it holds
+          const float w = p[h2 * kT + t];
+          o[c][h2] = w != 0.f ? fmaf(w, x, o[c][h2]) : o[c][h2];
+        }
+      }
+    }
+    __syncthreads();
+  }
+};
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads) k_attn_simt(const __grid_constant__ AttnArgs a) {
+  pdl_enter();
+  extern __shared__ __align__(16) float sm[];
+  const LatentCache& C = a.cache;
+  const int W = C.dc + C.dr;
+  Tile t{sm, sm + kNH * W, nullptr, nullptr, W, W + 1, 0, C.dc};
+  t.p = t.kv + kT * t.stride;
+  t.alpha = t.p + kNH * kT;
+  int64_t* row = reinterpret_cast<int64_t*>(sm + ((t.alpha + kNH - sm + 1) / 2 * 2));  // [kT] cache rows, -1: none
+  __shared__ int tmp[35];
+  __shared__ float norm[kNH];
+  const int g = blockIdx.x % a.ngroups, u = blockIdx.x / a.ngroups;
+  const int h0 = g * kNH, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int items = a.Q * a.rows;
+  const int total = attn_units_before(a, items, tmp), ranges = min(a.ranges, total);
+  if (u >= ranges) return;
+  const int my_begin = range_begin(total, ranges, u), stop = range_begin(total, ranges, u + 1);
+  int first;
+  int item = attn_item_of(a, my_begin, tmp, &first);
+  int at = my_begin;
+  while (at < stop) {
+    const int q = item / a.rows, r = item - q * a.rows;
+    const int end = attn_end(a, q, r);
+    if (end == 0 && threadIdx.x == 0) raise_error(a.err, ERR_CTX_LEN, q, (uint32_t)a.ctx_len[q]);
+    const int n = attn_tiles(a, end);
+    const int t0 = at - first, t1 = min(n, stop - first);
+    __syncthreads();
+    for (int i = threadIdx.x; i < kNH * W; i += kThreads) {
+      const int h = h0 + i / W, d = i % W;
+      float v = 0.f;
+      if (h < a.H)
+        v = d < C.dc ? to_f32(reinterpret_cast<const T*>(a.ql)[item * a.ql_tok + h * a.ql_head + d])
+                     : to_f32(reinterpret_cast<const T*>(a.qr)[item * a.qr_tok + h * a.qr_head + d - C.dc]);
+      t.q[i] = v;
+    }
+    float m = kNegInf, l = 0.f, o[2][kNH] = {};
+    for (int k = t0; k < t1; ++k) {
+      if (warp == 0) {
+        const int e = k * kT + lane;
+        int slot = -1;
+        if (a.list) {
+          if (e < a.topk) slot = a.list[(int64_t)item * a.topk + e];
+        } else {
+          slot = e;
+        }
+        row[lane] = (slot >= 0 && slot < end) ? cache_row(C, q, slot, a.err) : -1;
+      }
+      __syncthreads();
+      for (int i = threadIdx.x; i < kT * W; i += kThreads) {
+        const int j = i / W, d = i - j * W;
+        t.kv[j * t.stride + d] = row[j] >= 0 ? to_f32(reinterpret_cast<const T*>(C.data)[row[j] * W + d]) : 0.f;
+      }
+      const bool seen = row[lane] >= 0;
+      __syncthreads();
+      t.step(m, l, o, a.scale_log2, seen);
+    }
+    if (t0 == 0 && t1 == n) {
+      if (lane == 0) {
+        norm[warp] = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+        if (a.lse && h0 + warp < a.H)
+          a.lse[(int64_t)item * a.H + h0 + warp] = l == 0.f ? kNegInf : (m + log2f(l)) * (1.f / kLog2e);
+      }
+      __syncthreads();
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int d = threadIdx.x + c * kThreads;
+        if (d < C.dc)
+          for (int h = 0; h < kNH && h0 + h < a.H; ++h)
+            reinterpret_cast<T*>(a.out)[((int64_t)item * a.H + h0 + h) * C.dc + d] = from_f32<T>(o[c][h] * norm[h]);
+      }
+    } else {
+      const int64_t part = (int64_t)blockIdx.x * 2 + (first <= my_begin ? 0 : 1);
+      if (lane == 0) a.part_ml[part * kNH + warp] = make_float2(m, l);
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int d = threadIdx.x + c * kThreads;
+        if (d < C.dc)
+#pragma unroll
+          for (int h = 0; h < kNH; ++h) a.part[(part * kNH + h) * C.dc + d] = o[c][h];
+      }
+    }
+    at = first + t1;
+    first += n;
+    ++item;
+  }
+}
+
+// Joins the shares of an item that several blocks worked on: one block per
+// (item, head).
+template <typename T>
+__global__ void __launch_bounds__(128) k_attn_combine(const __grid_constant__ AttnArgs a) {
+  pdl_enter();
+  __shared__ int tmp[35];
+  const int item = blockIdx.y, h = blockIdx.x;
+  const int total = attn_units_before(a, a.Q * a.rows, tmp), ranges = min(a.ranges, total);
+  const int first = attn_units_before(a, item, tmp);
+  const int n = attn_tiles(a, attn_end(a, item / a.rows, item % a.rows));
+  const int u0 = range_of(total, ranges, first), u1 = range_of(total, ranges, first + n - 1);
+  if (u0 == u1) return;
+  const int g = h / a.group, hh = h - g * a.group, dc = a.cache.dc;
+  auto slot = [&](int u) {
+    return ((int64_t)(u * a.ngroups + g) * 2 + (first <= range_begin(total, ranges, u) ? 0 : 1)) * a.group + hh;
+  };
+  float m = kNegInf;
+  for (int u = u0; u <= u1; ++u) m = fmaxf(m, a.part_ml[slot(u)].x);
+  const float ref = m == kNegInf ? 0.f : m;
+  float l = 0.f;
+  for (int u = u0; u <= u1; ++u) {
+    const float2 ml = a.part_ml[slot(u)];
+    l += ml.y * exp2f(ml.x - ref);
+  }
+  const float norm = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+  for (int d = threadIdx.x; d < dc; d += blockDim.x) {
+    float o = 0.f;
+    for (int u = u0; u <= u1; ++u) {
+      const int64_t at = slot(u);
+      const float w = exp2f(a.part_ml[at].x - ref);
+      if (w != 0.f) o = fmaf(w, a.part[at * dc + d], o);
+    }
+    reinterpret_cast<T*>(a.out)[((int64_t)item * a.H + h) * dc + d] = from_f32<T>(o * norm);
+  }
+  if (threadIdx.x == 0 && a.lse)
+    a.lse[(int64_t)item * a.H + h] = l == 0.f ? kNegInf : (m + log2f(l)) * (1.f / kLog2e);
+}
+
+// ---------------------------------------------------------------------------
+// Expanded form
+// ---------------------------------------------------------------------------
+constexpr int kES = 32, kEK = 32;  // slots of a block, reduction step
+
+// kv[off + s][h] = W_h c_s for a tile of kES slots and one head; head 0 also
+// copies the shared key part.  grid (slot tiles, heads, requests).
+template <typename T>
+__global__ void __launch_bounds__(kThreads) k_expand_simt(const __grid_constant__ PrefillArgs a) {
+  pdl_enter();
+  extern __shared__ __align__(16) float sm[];
+  __shared__ int64_t tmp[33];
+  __shared__ int64_t row[kES];
+  const LatentCache& C = a.cache;
+  const int h = blockIdx.y, q = blockIdx.z, N = a.dn + a.dv, W = C.dc + C.dr;
+  const Chunk ch = prefill_chunk(a, q, blockIdx.x == 0 && h == 0 && threadIdx.x == 0);
+  if (ch.end == 0) return;
+  const int64_t off = prefill_rows_before(a, q, tmp);
+  if (off + ch.end > a.cap) {
+    if (blockIdx.x == 0 && h == 0 && threadIdx.x == 0) raise_error(a.err, ERR_CAPACITY, q, (uint32_t)ch.end);
+    return;
+  }
+  float* cs = sm;                  // [kEK][kES + 1]
+  float* ws = sm + kEK * (kES + 1);  // [N][kEK + 1]
+  for (int s0 = blockIdx.x * kES; s0 < ch.end; s0 += gridDim.x * kES) {
+    __syncthreads();
+    if (threadIdx.x < kES) {
+      const int slot = s0 + threadIdx.x;
+      row[threadIdx.x] = slot < ch.end ? cache_row(C, q, slot, a.err) : -1;
+    }
+    __syncthreads();
+    float acc[2][kES] = {};
+    for (int k0 = 0; k0 < C.dc; k0 += kEK) {
+      for (int i = threadIdx.x; i < kES * kEK; i += kThreads) {
+        const int s = i / kEK, k = i % kEK;
+        cs[k * (kES + 1) + s] = (row[s] >= 0 && k0 + k < C.dc)
+                                    ? to_f32(reinterpret_cast<const T*>(C.data)[row[s] * W + k0 + k]) : 0.f;
+      }
+      for (int i = threadIdx.x; i < N * kEK; i += kThreads) {
+        const int n = i / kEK, k = i % kEK;
+        ws[n * (kEK + 1) + k] = k0 + k < C.dc
+            ? to_f32(reinterpret_cast<const T*>(a.w)[((int64_t)h * N + n) * C.dc + k0 + k]) : 0.f;
+      }
+      __syncthreads();
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int n = threadIdx.x + c * kThreads;
+        if (n < N)
+          for (int k = 0; k < kEK; ++k) {
+            const float w = ws[n * (kEK + 1) + k];
+#pragma unroll
+            for (int s = 0; s < kES; ++s) acc[c][s] = fmaf(w, cs[k * (kES + 1) + s], acc[c][s]);
+          }
+      }
+      __syncthreads();
+    }
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const int n = threadIdx.x + c * kThreads;
+      if (n < N)
+#pragma unroll
+        for (int s = 0; s < kES; ++s)
+          if (s0 + s < ch.end)
+            reinterpret_cast<T*>(a.kv)[((off + s0 + s) * a.H + h) * N + n] = from_f32<T>(acc[c][s]);
+    }
+    if (h == 0)
+      for (int i = threadIdx.x; i < kES * C.dr; i += kThreads) {
+        const int s = i / C.dr, d = i - s * C.dr;
+        if (row[s] >= 0)
+          reinterpret_cast<T*>(a.kr)[(off + s0 + s) * C.dr + d] =
+              reinterpret_cast<const T*>(C.data)[row[s] * W + C.dc + d];
+      }
+  }
+}
+
+// Whether a page of the request's first `end` slots lies outside the cache
+// (all threads of the block).
+__device__ __forceinline__ bool bad_pages(const LatentCache& C, int q, int end) {
+  int bad = 0;
+  for (int i = threadIdx.x; i <= (end - 1) >> C.log2b; i += blockDim.x) {
+    const int page = C.bt[(int64_t)q * C.bt_stride + i];
+    bad |= page < 0 || page >= C.num_pages;
+  }
+  return __syncthreads_or(bad) != 0;
+}
+
+// Causal attention of kNH rows of one head.  grid (row tiles, heads, requests).
+template <typename T>
+__global__ void __launch_bounds__(kThreads) k_prefill_simt(const __grid_constant__ PrefillArgs a) {
+  pdl_enter();
+  extern __shared__ __align__(16) float sm[];
+  __shared__ int64_t tmp[33];
+  __shared__ float norm[kNH];
+  const int h = blockIdx.y, q = blockIdx.z, N = a.dn + a.dv, dr = a.cache.dr, W = a.dn + dr;
+  const Chunk ch = prefill_chunk(a, q, false);
+  if (ch.end == 0) return;
+  const int64_t off = prefill_rows_before(a, q, tmp);
+  if (off + ch.end > a.cap || bad_pages(a.cache, q, ch.end)) return;
+  Tile t{sm, sm + kNH * W, nullptr, nullptr, W, (W + a.dv) | 1, W, a.dv};
+  t.p = t.kv + kT * t.stride;
+  t.alpha = t.p + kNH * kT;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t token0 = (int64_t)q * a.rows;
+  for (int r0 = blockIdx.x * kNH; r0 < ch.count; r0 += gridDim.x * kNH) {
+    __syncthreads();
+    for (int i = threadIdx.x; i < kNH * W; i += kThreads) {
+      const int r = r0 + i / W, d = i % W;
+      t.q[i] = r < ch.count ? to_f32(reinterpret_cast<const T*>(a.q)[(token0 + r) * a.q_tok + h * a.q_head + d]) : 0.f;
+    }
+    const int pos = ch.ctx - 1 + r0 + warp;
+    const int last = min(ch.ctx - 1 + r0 + kNH - 1, ch.end - 1);
+    float m = kNegInf, l = 0.f, o[2][kNH] = {};
+    for (int j0 = 0; j0 <= last; j0 += kT) {
+      __syncthreads();
+      for (int i = threadIdx.x; i < kT * (W + a.dv); i += kThreads) {
+        const int j = i / (W + a.dv), d = i - j * (W + a.dv);
+        float v = 0.f;
+        if (j0 + j < ch.end) {
+          const int64_t s = off + j0 + j;
+          const T* kv = reinterpret_cast<const T*>(a.kv) + (s * a.H + h) * N;
+          v = to_f32(d < a.dn ? kv[d] : d < W ? reinterpret_cast<const T*>(a.kr)[s * dr + d - a.dn] : kv[d - dr]);
+        }
+        t.kv[j * t.stride + d] = v;
+      }
+      __syncthreads();
+      t.step(m, l, o, a.scale_log2, j0 + lane <= pos && j0 + lane <= last);
+    }
+    if (lane == 0) norm[warp] = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+    __syncthreads();
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const int d = threadIdx.x + c * kThreads;
+      if (d < a.dv)
+        for (int r = 0; r < kNH && r0 + r < ch.count; ++r)
+          reinterpret_cast<T*>(a.out)[((token0 + r0 + r) * a.H + h) * a.dv + d] = from_f32<T>(o[c][r] * norm[r]);
+    }
+  }
+}
+
+template <typename F>
+cudaError_t with_smem(F kernel, size_t smem) {
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+}
+
+}  // namespace
+
+cudaError_t launch_attn_simt(const AttnArgs& a, int bf16, cudaStream_t s) {
+  const int W = a.cache.dc + a.cache.dr;
+  const size_t smem = sizeof(float) * (kNH * W + kT * (W + 1) + kNH * kT + kNH + 2) + sizeof(int64_t) * kT;
+  auto kernel = bf16 ? k_attn_simt<__nv_bfloat16> : k_attn_simt<float>;
+  cudaError_t e = with_smem(kernel, smem);
+  if (e != cudaSuccess) return e;
+  PdlLaunch l(dim3((unsigned)(a.ranges * a.ngroups)), dim3(kThreads), smem, s);
+  return cudaLaunchKernelEx(&l.cfg, kernel, a);
+}
+
+cudaError_t launch_attn_combine(const AttnArgs& a, int bf16, cudaStream_t s) {
+  PdlLaunch l(dim3((unsigned)a.H, (unsigned)(a.Q * a.rows)), dim3(128), 0, s);
+  return bf16 ? cudaLaunchKernelEx(&l.cfg, k_attn_combine<__nv_bfloat16>, a)
+              : cudaLaunchKernelEx(&l.cfg, k_attn_combine<float>, a);
+}
+
+cudaError_t launch_expand_simt(const PrefillArgs& a, int bf16, cudaStream_t s) {
+  const size_t smem = sizeof(float) * (kEK * (kES + 1) + (size_t)(a.dn + a.dv) * (kEK + 1));
+  auto kernel = bf16 ? k_expand_simt<__nv_bfloat16> : k_expand_simt<float>;
+  cudaError_t e = with_smem(kernel, smem);
+  if (e != cudaSuccess) return e;
+  const int64_t tiles = ((int64_t)a.max_slots + kES - 1) / kES;
+  PdlLaunch l(dim3((unsigned)(tiles < 1024 ? tiles : 1024), (unsigned)a.H, (unsigned)a.Q), dim3(kThreads), smem, s);
+  return cudaLaunchKernelEx(&l.cfg, kernel, a);
+}
+
+cudaError_t launch_prefill_simt(const PrefillArgs& a, int bf16, cudaStream_t s) {
+  const int W = a.dn + a.cache.dr;
+  const size_t smem = sizeof(float) * (kNH * W + kT * ((W + a.dv) | 1) + kNH * kT + kNH);
+  auto kernel = bf16 ? k_prefill_simt<__nv_bfloat16> : k_prefill_simt<float>;
+  cudaError_t e = with_smem(kernel, smem);
+  if (e != cudaSuccess) return e;
+  const int64_t tiles = ((int64_t)a.rows + kNH - 1) / kNH;
+  PdlLaunch l(dim3((unsigned)(tiles < 4096 ? tiles : 4096), (unsigned)a.H, (unsigned)a.Q), dim3(kThreads), smem, s);
+  return cudaLaunchKernelEx(&l.cfg, kernel, a);
+}
+
+}  // namespace spin
