@@ -295,6 +295,9 @@ spin_status spin_latent_attention(spin_latent lt, int rows, const void* cache, i
   a.ql_head = ql_head_stride;
   a.qr_tok = qr_token_stride;
   a.qr_head = qr_head_stride;
+  const int64_t per16 = c.dtype == SPIN_BF16 ? 8 : 4;
+  a.q_vec = ((uintptr_t)q_latent & 15) == 0 && ((uintptr_t)q_rope & 15) == 0 && ql_token_stride % per16 == 0 &&
+            ql_head_stride % per16 == 0 && qr_token_stride % per16 == 0 && qr_head_stride % per16 == 0;
   a.scale_log2 = (float)((double)c.softmax_scale * 1.4426950408889634);
   a.out = out;
   a.lse = lse;
@@ -310,8 +313,15 @@ spin_status spin_latent_attention(spin_latent lt, int rows, const void* cache, i
     const int64_t n = a.list ? a.topk : a.max_slots;
     a.ranges = (int)std::min<int64_t>(std::max(1, blocks / a.ngroups), (int64_t)a.Q * rows * ((n + tile - 1) / tile));
   };
-  plan(kSimtTile, kSimtHeads, std::min(2 * lt->sms, kSimtBlocks));
-  cudaError_t e = launch_attn_simt(a, bf16, (cudaStream_t)stream);
+  cudaError_t e;
+  if (lt->encode_fn && attn_tc_supported(a, bf16)) {
+    const int groups = (a.H + kTcHeads - 1) / kTcHeads;
+    plan(kTcTile, ((a.H + groups - 1) / groups + 15) / 16 * 16, std::min(lt->sms, kTcBlocks));
+    e = launch_attn_tc(a, lt->encode_fn, (cudaStream_t)stream);
+  } else {
+    plan(kSimtTile, kSimtHeads, std::min(2 * lt->sms, kSimtBlocks));
+    e = launch_attn_simt(a, bf16, (cudaStream_t)stream);
+  }
   if (e == cudaSuccess) e = launch_attn_combine(a, bf16, (cudaStream_t)stream);
   return cuda_status(e);
 }

@@ -109,6 +109,7 @@ struct AttnArgs {
   const void* ql;
   const void* qr;
   int64_t ql_tok, ql_head, qr_tok, qr_head;
+  int q_vec;                 // every head of ql and qr starts on 16 bytes
   float scale_log2;          // softmax scale * log2(e)
   void* out;                 // [Q][rows][H][dc]
   float* lse;                // [Q][rows][H] or null
@@ -204,6 +205,8 @@ constexpr int kSimtHeads = 8, kSimtTile = 32, kSimtBlocks = 296;
 constexpr int kTcHeads = 64, kTcTile = 64, kTcBlocks = 148;
 
 cudaError_t launch_attn_simt(const AttnArgs& a, int bf16, cudaStream_t s);
+bool attn_tc_supported(const AttnArgs& a, int bf16);
+cudaError_t launch_attn_tc(const AttnArgs& a, void* encode_fn, cudaStream_t s);
 cudaError_t launch_attn_combine(const AttnArgs& a, int bf16, cudaStream_t s);
 
 // ---------------------------------------------------------------------------
