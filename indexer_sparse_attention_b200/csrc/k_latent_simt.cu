@@ -163,42 +163,102 @@ __global__ void __launch_bounds__(kThreads) k_attn_simt(const __grid_constant__ 
   }
 }
 
-// Joins the shares of an item that several blocks worked on: one block per
-// (item, head).
-template <typename T>
-__global__ void __launch_bounds__(128) k_attn_combine(const __grid_constant__ AttnArgs a) {
-  pdl_enter();
+// Joins the shares of an item that several blocks worked on, WPH warps per
+// (item, head) of kJoinWarps: warp i of a head takes shares i, i + WPH, ..,
+// and the warps' sums meet in warp order.  Bound by the shares' bytes, or for
+// one long context by the latency of its many shares (hence WPH = 8 there).
+constexpr int kJoinWarps = 8;
+
+template <typename T, int WPH>
+__global__ void __launch_bounds__(kJoinWarps * 32) k_attn_combine(const __grid_constant__ AttnArgs a) {
   __shared__ int tmp[35];
-  const int item = blockIdx.y, h = blockIdx.x;
+  __shared__ float4 sums[WPH > 1 ? kJoinWarps : 1][WPH > 1 ? 128 : 1];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int item = blockIdx.y, h = blockIdx.x * (kJoinWarps / WPH) + warp / WPH, mine = warp % WPH;
+  // The lengths were there before the attention kernel started, so the place
+  // of the shares is found while it still runs.
   const int total = attn_units_before(a, a.Q * a.rows, tmp), ranges = min(a.ranges, total);
   const int first = attn_units_before(a, item, tmp);
   const int n = attn_tiles(a, attn_end(a, item / a.rows, item % a.rows));
   const int u0 = range_of(total, ranges, first), u1 = range_of(total, ranges, first + n - 1);
-  if (u0 == u1) return;
+  pdl_enter();
+  if (u0 == u1 || h >= a.H) return;  // (WPH = 8: the same for all warps of the block)
   const int g = h / a.group, hh = h - g * a.group, dc = a.cache.dc;
   auto slot = [&](int u) {
     return ((int64_t)(u * a.ngroups + g) * 2 + (first <= range_begin(total, ranges, u) ? 0 : 1)) * a.group + hh;
   };
   float m = kNegInf;
-  for (int u = u0; u <= u1; ++u) m = fmaxf(m, a.part_ml[slot(u)].x);
+  for (int u = u0 + lane; u <= u1; u += 32) m = fmaxf(m, a.part_ml[slot(u)].x);
+#pragma unroll
+  for (int d = 16; d >= 1; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
   const float ref = m == kNegInf ? 0.f : m;
   float l = 0.f;
-  for (int u = u0; u <= u1; ++u) {
+  for (int u = u0 + lane; u <= u1; u += 32) {
     const float2 ml = a.part_ml[slot(u)];
     l += ml.y * exp2f(ml.x - ref);
   }
+#pragma unroll
+  for (int d = 16; d >= 1; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
   const float norm = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
-  for (int d = threadIdx.x; d < dc; d += blockDim.x) {
-    float o = 0.f;
-    for (int u = u0; u <= u1; ++u) {
-      const int64_t at = slot(u);
-      const float w = exp2f(a.part_ml[at].x - ref);
-      if (w != 0.f) o = fmaf(w, a.part[at * dc + d], o);
-    }
-    reinterpret_cast<T*>(a.out)[((int64_t)item * a.H + h) * dc + d] = from_f32<T>(o * norm);
-  }
-  if (threadIdx.x == 0 && a.lse)
+  if (mine == 0 && lane == 0 && a.lse)
     a.lse[(int64_t)item * a.H + h] = l == 0.f ? kNegInf : (m + log2f(l)) * (1.f / kLog2e);
+  // columns 4 (lane + 32 i) .. + 3
+  float4 o[4] = {};
+  constexpr int kAhead = 4;
+  for (int v = u0 + mine; v <= u1; v += WPH * kAhead) {
+    float wt[kAhead];
+    const float4* src[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      const int u = v + k * WPH;
+      const int64_t at = slot(min(u, u1));
+      wt[k] = u <= u1 ? exp2f(a.part_ml[at].x - ref) : 0.f;
+      src[k] = reinterpret_cast<const float4*>(a.part + at * dc);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int c = lane + 32 * i;
+      if (4 * c < dc) {
+        float4 x[kAhead];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) x[k] = wt[k] != 0.f ? src[k][c] : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+          o[i].x = fmaf(wt[k], x[k].x, o[i].x);
+          o[i].y = fmaf(wt[k], x[k].y, o[i].y);
+          o[i].z = fmaf(wt[k], x[k].z, o[i].z);
+          o[i].w = fmaf(wt[k], x[k].w, o[i].w);
+        }
+      }
+    }
+  }
+  auto store = [&](int c, float4 x) {
+    T* out = reinterpret_cast<T*>(a.out) + ((int64_t)item * a.H + h) * dc + 4 * c;
+    out[0] = from_f32<T>(x.x * norm);
+    out[1] = from_f32<T>(x.y * norm);
+    out[2] = from_f32<T>(x.z * norm);
+    out[3] = from_f32<T>(x.w * norm);
+  };
+  if constexpr (WPH == 1) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (4 * (lane + 32 * i) < dc) store(lane + 32 * i, o[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sums[warp][lane + 32 * i] = o[i];
+    __syncthreads();
+    for (int c = threadIdx.x; 4 * c < dc; c += kJoinWarps * 32) {
+      float4 x = sums[0][c];
+      for (int k = 1; k < kJoinWarps; ++k) {
+        const float4 y = sums[k][c];
+        x.x += y.x;
+        x.y += y.y;
+        x.z += y.z;
+        x.w += y.w;
+      }
+      store(c, x);
+    }
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -358,9 +418,13 @@ cudaError_t launch_attn_simt(const AttnArgs& a, int bf16, cudaStream_t s) {
 }
 
 cudaError_t launch_attn_combine(const AttnArgs& a, int bf16, cudaStream_t s) {
-  PdlLaunch l(dim3((unsigned)a.H, (unsigned)(a.Q * a.rows)), dim3(128), 0, s);
-  return bf16 ? cudaLaunchKernelEx(&l.cfg, k_attn_combine<__nv_bfloat16>, a)
-              : cudaLaunchKernelEx(&l.cfg, k_attn_combine<float>, a);
+  // an item's shares, at the even lengths of lists: a few for many items, else many
+  const bool many = a.ranges > 3 * a.Q * a.rows;
+  const int per = many ? 1 : kJoinWarps;
+  auto kernel = many ? (bf16 ? k_attn_combine<__nv_bfloat16, kJoinWarps> : k_attn_combine<float, kJoinWarps>)
+                     : (bf16 ? k_attn_combine<__nv_bfloat16, 1> : k_attn_combine<float, 1>);
+  PdlLaunch l(dim3((unsigned)((a.H + per - 1) / per), (unsigned)(a.Q * a.rows)), dim3(kJoinWarps * 32), 0, s);
+  return cudaLaunchKernelEx(&l.cfg, kernel, a);
 }
 
 cudaError_t launch_expand_simt(const PrefillArgs& a, int bf16, cudaStream_t s) {

@@ -20,14 +20,17 @@
 // what the outputs' own rounding costs as well); their sum is of the
 // unrounded ones.
 //
-// Warps (256 threads, one block per SM):
+// Warps (384 threads, one block per SM):
 //   0..3  softmax: S from TMEM (warp w: heads 16 w .. 16 w + 15), weights to
 //         shared memory; at an item's end O^T from TMEM to the output or to the
 //         block's share
-//   4     producer: list entries -> cache rows, gathered by TMA, four rows a
-//         request; entries are looked up two tiles ahead
-//   5     MMA issue (one lane), TMEM allocation
-//   6, 7  Q tile of the next item into shared memory
+//   4..7  producers: list entries -> cache rows (looked up two tiles ahead)
+//         -> 16-byte asynchronous copies, eight lanes a 128-byte line.  A
+//         gather by TMA (four rows a request) moved 2.0 TB/s from one warp's
+//         lanes and 4.3 TB/s from four warps, these copies 6.45 TB/s (64 rows of
+//         1152 bytes at random from 302 MB, 148 blocks)
+//   8, 9  issue of the first and of the second product
+//   10, 11 Q tile of the next item into shared memory
 // Two 72 KB token tiles in flight, each cut into five parts (the rotary part
 // and four of 128 latent columns) with their own barriers: a part is
 // reloaded as soon as the second product has read its columns, and S starts
@@ -50,33 +53,34 @@ constexpr int kStageBytes = kBlocks * kBlk;
 constexpr int kStages = 2;
 constexpr int kParts = 5;                        // 0..3: column blocks 2 p, 2 p + 1; 4: kr
 constexpr int kInfo = 4;                         // ring of tile infos
-constexpr int kThreads = 256;
+constexpr int kThreads = 384;
+constexpr int kProducers = 128, kMmaWarp = 8, kQThreads = 64;
 constexpr float kLazy = 8.0f;
 constexpr uint32_t kSCol = 256;                  // S buffers behind O^T's 4 * 64 columns
 constexpr uint32_t kTmemCols = 512;
 
 struct Info {
-  uint64_t mask;  // tokens attended to
-  int flags;      // 1: first tile of an item's share, 2: its last, 4: the block's last
-  int pad;
+  uint32_t even, odd;  // the even and the odd tokens that are attended to
+  int flags;           // 1: first tile of an item's share, 2: its last, 4: the block's last
 };
 
 struct Bars {
-  uint64_t full[kStages][kParts];   // TMA
+  uint64_t full[kStages][kParts];   // copies landed
   uint64_t empty[kStages][kParts];  // MMAs that read the part
   uint64_t info[kInfo];             // producer: tile info written
   uint64_t sfull[2];                // S complete
-  uint64_t pfull;                   // weights written (and S read, O rescaled)
+  uint64_t sfree[2];                // S read
+  uint64_t pfull;                   // weights written, O rescaled
   uint64_t pempty;                  // second product complete
   uint64_t qfull, qempty;
   uint64_t oempty;                  // O^T read out
-  uint64_t done;
+  uint64_t done[2];
 };
 
 struct Misc {
   Bars bars;
   Info info[kInfo];
-  float fac[kTcHeads];  // rescale factors, then 1 / sum
+  alignas(16) float fac[kTcHeads];  // rescale factors, then 1 / sum
   int tmp[35];
   uint32_t tmem;
   int abort_flag;
@@ -108,7 +112,7 @@ struct Walk {
 };
 
 __global__ void __launch_bounds__(kThreads, 1)
-    k_attn_tc(const __grid_constant__ AttnArgs a, const __grid_constant__ CUtensorMap map) {
+    k_attn_tc(const __grid_constant__ AttnArgs a) {
   pdl_enter();
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -140,36 +144,39 @@ __global__ void __launch_bounds__(kThreads, 1)
     ms.abort_flag = 0;
     for (int s = 0; s < kStages; ++s)
       for (int p = 0; p < kParts; ++p) {
-        mbar_init(bar(B.full[s][p]), 1);
+        mbar_init(bar(B.full[s][p]), kProducers);
         mbar_init(bar(B.empty[s][p]), 1);
       }
     for (int i = 0; i < kInfo; ++i) mbar_init(bar(B.info[i]), 1);
-    for (int i = 0; i < 2; ++i) mbar_init(bar(B.sfull[i]), 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(B.sfull[i]), 1);
+      mbar_init(bar(B.sfree[i]), 4);
+      mbar_init(bar(B.done[i]), 1);
+    }
     mbar_init(bar(B.pfull), 4);
     mbar_init(bar(B.pempty), 1);
-    mbar_init(bar(B.qfull), 64);
+    mbar_init(bar(B.qfull), kQThreads);
     mbar_init(bar(B.qempty), 1);
     mbar_init(bar(B.oempty), 4);
-    mbar_init(bar(B.done), 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 5) tmem_alloc(smem_u32(&ms.tmem), kTmemCols);
+  if (warp == kMmaWarp) tmem_alloc(smem_u32(&ms.tmem), kTmemCols);
   fence_before();
   __syncthreads();
   fence_after();
   const uint32_t tmem = ms.tmem;
 
-  if (warp == 4) {
-    // ======================= producer (whole warp) =======================
-    // Lane l asks for tokens 4 (l % 16) .. + 3 of a tile; lanes 16.. take the
-    // second column block of a part.
+  if (warp >= 4 && warp < kMmaWarp) {
+    // ======================= producers =======================
+    // Each warp looks up all 64 tokens (lane l: 2 l, 2 l + 1), so that all
+    // agree on which tiles are passed over; it copies tokens 4 pw + l / 8 + 16 j,
+    // piece l % 8 of each 128-byte line.
     const LatentCache& C = a.cache;
-    const int tg = lane & 15;
-    const int none = C.num_pages << C.log2b;  // a row outside the cache: zeros
+    const int pw = warp - 4;
     struct Look {      // one unit of the stream
       int q, end, flags;
-      int slot[4];     // entries (list) or slots
-      int page[4];
+      int slot[2];     // entries (list) or slots
+      int page[2];
     };
     // stage 1: the unit's entries
     auto entries = [&](Look& x, bool& more) {
@@ -181,9 +188,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       x.q = w.q;
       x.end = w.end;
       x.flags = (k == w.t1 - 1 ? 2 : 0) | (w.at + 1 == w.stop ? 4 : 0);
-      const int e0 = k * kTok + 4 * tg;
+      const int e0 = k * kTok + 2 * lane;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < 2; ++i) {
         x.slot[i] = -1;
         if (a.list) {
           if (e0 + i < a.topk) x.slot[i] = __ldg(a.list + (int64_t)w.item * a.topk + e0 + i);
@@ -205,7 +212,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (x.q < 0) return;
       const int32_t* bt = C.bt + (int64_t)x.q * C.bt_stride;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < 2; ++i) {
         if (x.slot[i] >= x.end) x.slot[i] = -1;
         x.page[i] = x.slot[i] >= 0 ? __ldg(bt + (x.slot[i] >> C.log2b)) : 0;
       }
@@ -217,55 +224,62 @@ __global__ void __launch_bounds__(kThreads, 1)
     entries(x1, more);
     pages(x0);
     int tile = 0;
-    uint32_t armed[kStages][kParts];
-    for (int s = 0; s < kStages; ++s)
-      for (int p = 0; p < kParts; ++p) armed[s][p] = 2;
     bool ok = true, fresh = true;
+    const char* base = reinterpret_cast<const char*>(C.data) + (lane & 7) * 16;
     while (x0.q >= 0) {
       entries(x2, more);
       pages(x1);
       // rows and mask of x0
-      int row[4];
-      uint32_t nib = 0;
+      int row[2];
+      bool live[2];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        bool live = x0.slot[i] >= 0;
-        if (live && (x0.page[i] < 0 || x0.page[i] >= C.num_pages)) {
-          if (lane < 16) raise_error(a.err, ERR_PAGE, x0.q, (uint32_t)x0.page[i]);
-          live = false;
+      for (int i = 0; i < 2; ++i) {
+        live[i] = x0.slot[i] >= 0;
+        if (live[i] && (x0.page[i] < 0 || x0.page[i] >= C.num_pages)) {
+          if (pw == 0) raise_error(a.err, ERR_PAGE, x0.q, (uint32_t)x0.page[i]);
+          live[i] = false;
         }
-        row[i] = live ? (x0.page[i] << C.log2b) + (x0.slot[i] & (C.b - 1)) : none;
-        nib |= (uint32_t)live << i;
+        row[i] = live[i] ? (x0.page[i] << C.log2b) + (x0.slot[i] & (C.b - 1)) : -1;
       }
-      const uint32_t lo = __reduce_or_sync(0xffffffffu, tg < 8 ? nib << (4 * tg) : 0u);
-      const uint32_t hi = __reduce_or_sync(0xffffffffu, tg >= 8 ? nib << (4 * (tg - 8)) : 0u);
-      if (lo || hi || (x0.flags & 2)) {  // a tile of which nothing is attended to is passed over
+      const uint32_t even = __ballot_sync(0xffffffffu, live[0]), odd = __ballot_sync(0xffffffffu, live[1]);
+      if (even || odd || (x0.flags & 2)) {  // a tile of which nothing is attended to is passed over
         const int st = tile % kStages;
         const uint32_t par = (uint32_t)(tile / kStages) & 1u;
-        const uint32_t stage_at = kv_at + st * kStageBytes;
+        const char* src[4];
+        uint32_t dst[4], bytes[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int t = 4 * pw + (lane >> 3) + 16 * j;
+          const int r0 = __shfl_sync(0xffffffffu, row[0], t >> 1), r1 = __shfl_sync(0xffffffffu, row[1], t >> 1);
+          const int r = (t & 1) ? r1 : r0;
+          bytes[j] = r >= 0 ? 16u : 0u;  // 0: filled with zeros, nothing is read
+          src[j] = base + (int64_t)(r >= 0 ? r : 0) * (kW * 2);
+          dst[j] = kv_at + st * kStageBytes + t * 128 + (((lane & 7) ^ (t & 7)) << 4);
+        }
 #pragma unroll
         for (int j = 0; j < kParts; ++j) {
           const int p = j == 0 ? 4 : j - 1;  // kr first: S starts with it
-          if (lane == 0) {
-            ok = wait(bar(B.empty[st][p]), par ^ 1u, ctl);
-            if (ok) {
-              if (j == 0) {
-                // S of tile - 2 has been issued, so the softmax is past tile - 4, the slot's last user
-                Info& f = ms.info[tile % kInfo];
-                f.mask = (uint64_t)hi << 32 | lo;
-                f.flags = x0.flags | (fresh ? 1 : 0);
-                mbar_arrive(bar(B.info[tile % kInfo]));
-              }
-              mbar_expect_tx(bar(B.full[st][p]), p == 4 ? kBlk : 2 * kBlk);
-              armed[st][p] = par;
-            }
-          }
-          ok = __shfl_sync(0xffffffffu, ok, 0);
+          ok = wait_warp(bar(B.empty[st][p]), par ^ 1u, ctl);
           if (!ok) break;
-          const int blk = p == 4 ? 8 : 2 * p + (lane >> 4);
-          if (p != 4 || lane < 16)
-            tma_gather4(stage_at + blk * kBlk + tg * 512, &map, bar(B.full[st][p]), blk * 64, row[0], row[1], row[2],
-                        row[3]);
+          if (j == 0 && pw == 0 && lane == 0) {
+            // the second product of tile - 4, the slot's last user, is done: tile - 2 took its stage
+            Info& f = ms.info[tile % kInfo];
+            f.even = even;
+            f.odd = odd;
+            f.flags = x0.flags | (fresh ? 1 : 0);
+            mbar_arrive(bar(B.info[tile % kInfo]));
+          }
+#pragma unroll
+          for (int b = 0; b < (p == 4 ? 1 : 2); ++b) {
+            const int blk = p == 4 ? 8 : 2 * p + b;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst[i] + blk * kBlk),
+                           "l"(src[i] + blk * 128), "r"(bytes[i])
+                           : "memory");
+          }
+          // arrives when this thread's copies so far have landed
+          asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar(B.full[st][p])) : "memory");
         }
         if (!ok) break;
         fresh = x0.flags & 2;
@@ -274,107 +288,89 @@ __global__ void __launch_bounds__(kThreads, 1)
       x0 = x1;
       x1 = x2;
     }
-    if (lane == 0 && ms.abort_flag)
-      for (int s = 0; s < kStages; ++s)
-        for (int p = 0; p < kParts; ++p)
-          if (armed[s][p] < 2) drain(bar(B.full[s][p]), armed[s][p]);
-  } else if (warp == 5) {
-    // ======================= MMA issue =======================
-    if (lane == 0) {
-      const uint32_t id_s = idesc_bf16(64, kTok, 0, 0), id_o = idesc_bf16(128, NH, 1, 0);
-      int s_tile = 0, s_part = 0;  // next part of S to issue
-      int o_tile = 0;              // next second product
-      int s_seg = 0, o_seg = 0;
-      int s_flags = 0, s_total = 1 << 30;  // tiles there are, known once the last is seen
-      int flags_of[2] = {0, 0};
-      bool opened = false;
-      uint64_t t0 = gtimer();
-      uint32_t idle = 0;
-      while (o_tile < s_total) {
-        bool moved = false;
-        // the second product of o_tile, once its weights are there
-        if (o_tile < s_tile && mbar_test(bar(B.pfull), (uint32_t)o_tile & 1u)) {
-          const int fl = flags_of[o_tile & 1];
-          bool go = true;
-          if ((fl & 1) && o_seg > 0) go = wait(bar(B.oempty), (uint32_t)(o_seg - 1) & 1u, ctl);
-          if (!go) break;
-          fence_after();
-          const int st = o_tile % kStages;
-          const uint32_t stage_at = kv_at + st * kStageBytes;
+    asm volatile("cp.async.wait_all;" ::: "memory");
+  } else if (warp == kMmaWarp) {
+    // ======================= first product =======================
+    // The whole warp runs the loop; the elected lane issues.  The two
+    // products are issued by two warps, each waiting for its own operands:
+    // one warp that polled for both spent more time polling than the MMAs take.
+    const uint32_t id_s = idesc_bf16(64, kTok, 0, 0);
+    const uint64_t a2 = (uint64_t)(NH * 128 >> 4), b2 = kBlk >> 4;
+    int seg = 0, flags = 0;
+    bool ok = true;
+    for (int tile = 0; ok && !(flags & 4); ++tile) {
+      const int st = tile % kStages;
+      ok = wait_warp(bar(B.info[tile % kInfo]), (uint32_t)(tile / kInfo) & 1u, ctl);
+      if (!ok) break;
+      flags = __shfl_sync(0xffffffffu, ms.info[tile % kInfo].flags, 0);
+      if (flags & 1) ok = wait_warp(bar(B.qfull), (uint32_t)seg & 1u, ctl);
+      // S's buffer is that of two tiles ago
+      if (ok && tile >= 2) ok = wait_warp(bar(B.sfree[tile & 1]), (uint32_t)((tile >> 1) - 1) & 1u, ctl);
+      const uint32_t d = tmem + kSCol + (uint32_t)(tile & 1) * kTok;
 #pragma unroll
-          for (int mb = 0; mb < 4; ++mb) {
-            const uint64_t ad = sw128_desc(stage_at + 2 * mb * kBlk, kBlk, 1024);
-            const uint64_t bd = sw128_desc(p_at, 16, 1024);
+      for (int j = 0; j < kParts; ++j) {
+        const int p = j == 0 ? 4 : j - 1;
+        ok = ok && wait_warp(bar(B.full[st][p]), (uint32_t)(tile / kStages) & 1u, ctl);
+        if (!ok) break;
+        fence_async_smem();  // the copies are generic-proxy writes, the MMAs read through the async proxy
+        fence_after();
+        const uint64_t ad = sw128_desc(q_at + 2 * p * NH * 128, 16, 1024);
+        const uint64_t bd = sw128_desc(kv_at + st * kStageBytes + 2 * p * kBlk, 16, 1024);
+        if (elect()) {
 #pragma unroll
-            for (int kk = 0; kk < kTok / 16; ++kk)
-              mma_f16(tmem + mb * NH, ad + kk * (2048 >> 4), bd + kk * 2, id_o, (kk > 0 || !(fl & 1)) ? 1u : 0u);
-            commit(bar(B.empty[st][mb]));
+          for (int kk = 0; kk < 4; ++kk) mma_f16(d, ad + 2 * kk, bd + 2 * kk, id_s, j > 0 || kk > 0 ? 1u : 0u);
+          if (p == 4) {
+            commit(bar(B.empty[st][4]));
+          } else {
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) mma_f16(d, ad + a2 + 2 * kk, bd + b2 + 2 * kk, id_s, 1u);
           }
-          commit(bar(B.pempty));
-          if (fl & 2) ++o_seg;
-          ++o_tile;
-          moved = true;
-        }
-        // parts of S that have landed.  S's buffer is that of two tiles ago,
-        // whose weights have been taken (o_tile has passed it)
-        if (s_tile < s_total && s_tile <= o_tile + 1) {
-          bool ready = true;
-          if (!opened) {
-            ready = mbar_test(bar(B.info[s_tile % kInfo]), (uint32_t)(s_tile / kInfo) & 1u);
-            if (ready) {
-              s_flags = ms.info[s_tile % kInfo].flags;
-              if (s_flags & 1) ready = mbar_test(bar(B.qfull), (uint32_t)s_seg & 1u);
-              opened = ready;
-            }
-          }
-          const int st = s_tile % kStages;
-          const int p = s_part == 0 ? 4 : s_part - 1;
-          if (ready && mbar_test(bar(B.full[st][p]), (uint32_t)(s_tile / kStages) & 1u)) {
-            fence_after();
-            const uint32_t d = tmem + kSCol + (uint32_t)(s_tile & 1) * kTok;
-            const int b0 = p == 4 ? 8 : 2 * p, b1 = p == 4 ? 9 : 2 * p + 2;
-            for (int blk = b0; blk < b1; ++blk) {
-              const uint64_t ad = sw128_desc(q_at + blk * NH * 128, 16, 1024);
-              const uint64_t bd = sw128_desc(kv_at + st * kStageBytes + blk * kBlk, 16, 1024);
-#pragma unroll
-              for (int kk = 0; kk < 4; ++kk)
-                mma_f16(d, ad + 2 * kk, bd + 2 * kk, id_s, (s_part > 0 || kk > 0) ? 1u : 0u);
-            }
-            if (p == 4) commit(bar(B.empty[st][4]));
-            if (++s_part == kParts) {
-              commit(bar(B.sfull[s_tile & 1]));
-              if (s_flags & 2) {
-                commit(bar(B.qempty));
-                ++s_seg;
-              }
-              flags_of[s_tile & 1] = s_flags;
-              if (s_flags & 4) s_total = s_tile + 1;
-              ++s_tile;
-              s_part = 0;
-              opened = false;
-            }
-            moved = true;
+          if (j == kParts - 1) {
+            commit(bar(B.sfull[tile & 1]));
+            if (flags & 2) commit(bar(B.qempty));
           }
         }
-        if (moved) {
-          idle = 0;
-        } else if ((++idle & 255u) == 0) {
-          if (*ctl.abort_flag) break;
-          if (idle == 256) t0 = gtimer();
-          if (gtimer() - t0 > kTimeoutNs) {
-            *ctl.abort_flag = 1;
-            raise_error(a.err, ERR_TIMEOUT, blockIdx.x, 5);
-            break;
-          }
-        }
+        __syncwarp();
       }
-      // every MMA is complete before TMEM is given back
-      commit(bar(B.done));
-      drain(bar(B.done), 0);
+      if (flags & 2) ++seg;
     }
-  } else if (warp >= 6) {
+    // every MMA is complete before TMEM is given back
+    if (elect()) commit(bar(B.done[0]));
+    __syncwarp();
+    drain(bar(B.done[0]), 0);
+  } else if (warp == kMmaWarp + 1) {
+    // ======================= second product =======================
+    const uint32_t id_o = idesc_bf16(128, NH, 1, 0);
+    int seg = 0, flags = 0;
+    for (int tile = 0; !(flags & 4); ++tile) {
+      const int st = tile % kStages;
+      if (!wait_warp(bar(B.info[tile % kInfo]), (uint32_t)(tile / kInfo) & 1u, ctl)) break;
+      flags = __shfl_sync(0xffffffffu, ms.info[tile % kInfo].flags, 0);
+      if (!wait_warp(bar(B.pfull), (uint32_t)tile & 1u, ctl)) break;
+      if ((flags & 1) && seg > 0 && !wait_warp(bar(B.oempty), (uint32_t)(seg - 1) & 1u, ctl)) break;
+      fence_after();
+      const uint64_t ad = sw128_desc(kv_at + st * kStageBytes, kBlk, 1024), bd = sw128_desc(p_at, 16, 1024);
+      const uint32_t joined = !(flags & 1);
+      if (elect()) {
+#pragma unroll
+        for (int mb = 0; mb < 4; ++mb) {
+#pragma unroll
+          for (int kk = 0; kk < kTok / 16; ++kk)
+            mma_f16(tmem + mb * NH, ad + mb * (2 * kBlk >> 4) + kk * (2048 >> 4), bd + kk * 2, id_o,
+                    kk > 0 ? 1u : joined);
+          commit(bar(B.empty[st][mb]));
+        }
+        commit(bar(B.pempty));
+      }
+      __syncwarp();
+      if (flags & 2) ++seg;
+    }
+    if (elect()) commit(bar(B.done[1]));
+    __syncwarp();
+    drain(bar(B.done[1]), 0);
+  } else if (warp > kMmaWarp + 1) {
     // ======================= Q tiles =======================
-    const int t = threadIdx.x - 6 * 32;
+    const int t = threadIdx.x - (kMmaWarp + 2) * 32;
     bool more = true;
     for (int seg = 0; more; ++seg) {
       w.open(a);
@@ -382,7 +378,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const char* ql = reinterpret_cast<const char*>(a.ql) + (int64_t)w.item * a.ql_tok * 2;
       const char* qr = reinterpret_cast<const char*>(a.qr) + (int64_t)w.item * a.qr_tok * 2;
       // 16-byte pieces: 72 a head, piece c of head h at block c / 8, row h, place (c % 8) ^ (h % 8)
-      for (int i = t; i < NH * (kW / 8); i += 64) {
+      for (int i = t; i < NH * (kW / 8); i += kQThreads) {
         const int h = i / (kW / 8), c = i - h * (kW / 8);
         const uint32_t dst = q_at + (uint32_t)((c >> 3) * NH * 128 + h * 128 + (((c & 7) ^ (h & 7)) << 4));
         if (h0 + h < H) {
@@ -428,24 +424,30 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool ok = wait_warp(bar(B.info[tile % kInfo]), (uint32_t)(tile / kInfo) & 1u, ctl);
         ok = ok && wait_warp(bar(B.sfull[tile & 1]), (uint32_t)(tile >> 1) & 1u, ctl);
         uint32_t s[32];
-        uint64_t mask = 0;
+        uint32_t even = 0, odd = 0;
         flags = 0;
         float t0 = -INFINITY, t1 = -INFINITY;
         if (ok) {
-          mask = ms.info[tile % kInfo].mask;
+          even = ms.info[tile % kInfo].even;
+          odd = ms.info[tile % kInfo].odd;
           flags = ms.info[tile % kInfo].flags;
         }
         if (ok && mine) {
           fence_after();
           tmem_ld_16x256b_x8(tmem + lanes + kSCol + (uint32_t)(tile & 1) * kTok, s);
           tmem_wait_ld();
-          if (mask != ~0ull) {
-            const uint64_t mm = mask >> (2 * (lane & 3));
+          fence_before();
+        }
+        __syncwarp();
+        if (ok && lane == 0) mbar_arrive(bar(B.sfree[tile & 1]));
+        if (ok && mine) {
+          if ((even & odd) != 0xffffffffu) {
+            // columns 8 n + 2 (lane % 4) and the next: bit 4 n + lane % 4 of the two
+            const uint32_t ev = even >> (lane & 3), od = odd >> (lane & 3);
 #pragma unroll
             for (int n = 0; n < 8; ++n) {
-              const uint32_t two = (uint32_t)(mm >> (8 * n));
-              if (!(two & 1)) s[4 * n] = s[4 * n + 2] = 0xff800000u;
-              if (!(two & 2)) s[4 * n + 1] = s[4 * n + 3] = 0xff800000u;
+              if (!(ev >> (4 * n) & 1)) s[4 * n] = s[4 * n + 2] = 0xff800000u;
+              if (!(od >> (4 * n) & 1)) s[4 * n + 1] = s[4 * n + 3] = 0xff800000u;
             }
           }
 #pragma unroll
@@ -597,26 +599,23 @@ __global__ void __launch_bounds__(kThreads, 1)
   fence_before();
   __syncthreads();
   fence_after();
-  if (warp == 5) tmem_dealloc(tmem, kTmemCols);
+  if (warp == kMmaWarp) tmem_dealloc(tmem, kTmemCols);
 }
 
 }  // namespace
 
 bool attn_tc_supported(const AttnArgs& a, int bf16) {
-  // cache rows are the tensor map's 32-bit coordinates, one past the last among them
+  // cache rows are 32-bit numbers
   return bf16 && a.cache.dc == kDC && a.cache.dr == kDR && ((uintptr_t)a.cache.data & 15) == 0 &&
-         ((int64_t)a.cache.num_pages << a.cache.log2b) < (int64_t(1) << 31) - 1 && ((uintptr_t)a.out & 3) == 0;
+         ((int64_t)a.cache.num_pages << a.cache.log2b) < (int64_t(1) << 31) && ((uintptr_t)a.out & 3) == 0;
 }
 
-cudaError_t launch_attn_tc(const AttnArgs& a, void* encode_fn, cudaStream_t s) {
-  CUtensorMap map;
-  const uint64_t rows = (uint64_t)a.cache.num_pages << a.cache.log2b;
-  if (!encode_fn || !encode_rows(encode_fn, &map, a.cache.data, rows, kW, kW * 2, 1)) return cudaErrorInvalidValue;
+cudaError_t launch_attn_tc(const AttnArgs& a, cudaStream_t s) {
   const uint32_t smem = smem_bytes(a.group);
   cudaError_t e = cudaFuncSetAttribute(k_attn_tc, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   PdlLaunch l(dim3((unsigned)(a.ranges * a.ngroups)), dim3(kThreads), smem, s);
-  return cudaLaunchKernelEx(&l.cfg, k_attn_tc, a, map);
+  return cudaLaunchKernelEx(&l.cfg, k_attn_tc, a);
 }
 
 }  // namespace spin

@@ -314,10 +314,10 @@ spin_status spin_latent_attention(spin_latent lt, int rows, const void* cache, i
     a.ranges = (int)std::min<int64_t>(std::max(1, blocks / a.ngroups), (int64_t)a.Q * rows * ((n + tile - 1) / tile));
   };
   cudaError_t e;
-  if (lt->encode_fn && attn_tc_supported(a, bf16)) {
+  if (attn_tc_supported(a, bf16)) {
     const int groups = (a.H + kTcHeads - 1) / kTcHeads;
     plan(kTcTile, ((a.H + groups - 1) / groups + 15) / 16 * 16, std::min(lt->sms, kTcBlocks));
-    e = launch_attn_tc(a, lt->encode_fn, (cudaStream_t)stream);
+    e = launch_attn_tc(a, (cudaStream_t)stream);
   } else {
     plan(kSimtTile, kSimtHeads, std::min(2 * lt->sms, kSimtBlocks));
     e = launch_attn_simt(a, bf16, (cudaStream_t)stream);

@@ -206,7 +206,7 @@ constexpr int kTcHeads = 64, kTcTile = 64, kTcBlocks = 148;
 
 cudaError_t launch_attn_simt(const AttnArgs& a, int bf16, cudaStream_t s);
 bool attn_tc_supported(const AttnArgs& a, int bf16);
-cudaError_t launch_attn_tc(const AttnArgs& a, void* encode_fn, cudaStream_t s);
+cudaError_t launch_attn_tc(const AttnArgs& a, cudaStream_t s);
 cudaError_t launch_attn_combine(const AttnArgs& a, int bf16, cudaStream_t s);
 
 // ---------------------------------------------------------------------------

@@ -102,6 +102,22 @@ __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, Ctl c) {
 __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, Ctl c) {
   return __all_sync(0xffffffffu, wait(bar, parity, c));
 }
+__device__ __forceinline__ bool test_warp(uint32_t bar, uint32_t parity) {
+  return __all_sync(0xffffffffu, mbar_test(bar, parity));
+}
+// One lane of a converged warp.  tcgen05.mma and its descriptors live on the
+// uniform datapath: issued by the elected lane of a warp whose control flow
+// is uniform, an instruction costs a few cycles; issued under `lane == 0` it
+// cost 80 to 160.
+__device__ __forceinline__ bool elect() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
+}
 // Waits for a copy in flight after an abort.
 __device__ __forceinline__ void drain(uint32_t bar, uint32_t parity) {
   const uint64_t t0 = gtimer();
