@@ -174,7 +174,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_attn_combine(const __grid_c
   __shared__ int tmp[35];
   __shared__ float4 sums[WPH > 1 ? kJoinWarps : 1][WPH > 1 ? 128 : 1];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int item = blockIdx.y, h = blockIdx.x * (kJoinWarps / WPH) + warp / WPH, mine = warp % WPH;
+  const int item = a.whole * a.ranges + blockIdx.y, h = blockIdx.x * (kJoinWarps / WPH) + warp / WPH, mine = warp % WPH;
   // The lengths were there before the attention kernel started, so the place
   // of the shares is found while it still runs.
   const int total = attn_units_before(a, a.Q * a.rows, tmp), ranges = min(a.ranges, total);
@@ -184,8 +184,10 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_attn_combine(const __grid_c
   pdl_enter();
   if (u0 == u1 || h >= a.H) return;  // (WPH = 8: the same for all warps of the block)
   const int g = h / a.group, hh = h - g * a.group, dc = a.cache.dc;
+  // the item starts inside its first block's range, or with it; it ran on into the others'
+  const int head = first == range_begin(total, ranges, u0) ? 0 : 1;
   auto slot = [&](int u) {
-    return ((int64_t)(u * a.ngroups + g) * 2 + (first <= range_begin(total, ranges, u) ? 0 : 1)) * a.group + hh;
+    return ((int64_t)(u * a.ngroups + g) * 2 + (u == u0 ? head : 0)) * a.group + hh;
   };
   float m = kNegInf;
   for (int u = u0 + lane; u <= u1; u += 32) m = fmaxf(m, a.part_ml[slot(u)].x);
@@ -419,11 +421,12 @@ cudaError_t launch_attn_simt(const AttnArgs& a, int bf16, cudaStream_t s) {
 
 cudaError_t launch_attn_combine(const AttnArgs& a, int bf16, cudaStream_t s) {
   // an item's shares, at the even lengths of lists: a few for many items, else many
-  const bool many = a.ranges > 3 * a.Q * a.rows;
+  const int items = a.Q * a.rows - a.whole * a.ranges;
+  const bool many = a.ranges > 3 * items;
   const int per = many ? 1 : kJoinWarps;
   auto kernel = many ? (bf16 ? k_attn_combine<__nv_bfloat16, kJoinWarps> : k_attn_combine<float, kJoinWarps>)
                      : (bf16 ? k_attn_combine<__nv_bfloat16, 1> : k_attn_combine<float, 1>);
-  PdlLaunch l(dim3((unsigned)((a.H + per - 1) / per), (unsigned)(a.Q * a.rows)), dim3(kJoinWarps * 32), 0, s);
+  PdlLaunch l(dim3((unsigned)((a.H + per - 1) / per), (unsigned)items), dim3(kJoinWarps * 32), 0, s);
   return cudaLaunchKernelEx(&l.cfg, kernel, a);
 }
 

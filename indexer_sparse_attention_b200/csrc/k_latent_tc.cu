@@ -20,17 +20,19 @@
 // what the outputs' own rounding costs as well); their sum is of the
 // unrounded ones.
 //
-// Warps (384 threads, one block per SM):
-//   0..3  softmax: S from TMEM (warp w: heads 16 w .. 16 w + 15), weights to
-//         shared memory; at an item's end O^T from TMEM to the output or to the
-//         block's share
-//   4..7  producers: list entries -> cache rows (looked up two tiles ahead)
-//         -> 16-byte asynchronous copies, eight lanes a 128-byte line.  A
+// Warps (480 threads, one block per SM):
+//   0..7  softmax: S from TMEM (warp w: heads 16 (w % 4) .. + 15, tokens
+//         32 (w / 4) .. + 31), weights to shared memory; at an item's end O^T
+//         from TMEM to the output or to the block's share
+//   8..11 producers: 16-byte asynchronous copies, eight lanes a 128-byte line.  A
 //         gather by TMA (four rows a request) moved 2.0 TB/s from one warp's
 //         lanes and 4.3 TB/s from four warps, these copies 6.45 TB/s (64 rows of
-//         1152 bytes at random from 302 MB, 148 blocks)
-//   8, 9  issue of the first and of the second product
-//   10, 11 Q tile of the next item into shared memory
+//         1152 bytes at random from 302 MB, 148 blocks).  An item's queries
+//         come the same way, as a tile whose rows are its heads
+//   12, 13  issue of the first and of the second product
+//   14    look-up, up to four tiles ahead: list entries -> pages -> cache rows,
+//         which it also asks into L2 (a tile's copies then take 1580 cycles under
+//         load, not 2450 to 3350)
 // Two 72 KB token tiles in flight, each cut into five parts (the rotary part
 // and four of 128 latent columns) with their own barriers: a part is
 // reloaded as soon as the second product has read its columns, and S starts
@@ -53,8 +55,9 @@ constexpr int kStageBytes = kBlocks * kBlk;
 constexpr int kStages = 2;
 constexpr int kParts = 5;                        // 0..3: column blocks 2 p, 2 p + 1; 4: kr
 constexpr int kInfo = 4;                         // ring of tile infos
-constexpr int kThreads = 384;
-constexpr int kProducers = 128, kMmaWarp = 8, kQThreads = 64;
+constexpr int kThreads = 480;
+constexpr int kSoft = 256, kProducers = 128;  // threads of the softmax and of the copies
+constexpr int kCopyWarp = 8, kMmaWarp = 12, kLookWarp = 14;
 constexpr float kLazy = 8.0f;
 constexpr uint32_t kSCol = 256;                  // S buffers behind O^T's 4 * 64 columns
 constexpr uint32_t kTmemCols = 512;
@@ -62,12 +65,15 @@ constexpr uint32_t kTmemCols = 512;
 struct Info {
   uint32_t even, odd;  // the even and the odd tokens that are attended to
   int flags;           // 1: first tile of an item's share, 2: its last, 4: the block's last
+  int item;
+  int row[kTok];       // cache rows, -1: not attended to
 };
 
 struct Bars {
   uint64_t full[kStages][kParts];   // copies landed
   uint64_t empty[kStages][kParts];  // MMAs that read the part
-  uint64_t info[kInfo];             // producer: tile info written
+  uint64_t info[kInfo];             // tile info written
+  uint64_t infofree[kInfo];         // and no longer needed: the tile's second product is complete
   uint64_t sfull[2];                // S complete
   uint64_t sfree[2];                // S read
   uint64_t pfull;                   // weights written, O rescaled
@@ -81,7 +87,6 @@ struct Misc {
   Bars bars;
   Info info[kInfo];
   alignas(16) float fac[kTcHeads];  // rescale factors, then 1 / sum
-  int tmp[35];
   uint32_t tmem;
   int abort_flag;
 };
@@ -91,23 +96,31 @@ __host__ __device__ constexpr uint32_t smem_bytes(int nh) {
 }
 static_assert(smem_bytes(kTcHeads) <= 227 * 1024, "one block's shared memory");
 
-// The walk over a block's shares of items: units [at, stop).
+// The walk over a block's items: `whole` of them whole, then its units [at,
+// stop) of the others, of which the current item starts at unit `first`.
 struct Walk {
-  int item, first, at, stop;
+  int item, whole, later;  // later: the first item that is not whole
+  int first, at, stop;
   int q, r, end, n, t0, t1;
   __device__ __forceinline__ void open(const AttnArgs& a) {
     q = item / a.rows;
     r = item - q * a.rows;
     end = attn_end(a, q, r);
     n = attn_tiles(a, end);
-    t0 = at - first;
-    t1 = min(n, stop - first);
+    t0 = whole > 0 ? 0 : at - first;
+    t1 = whole > 0 ? n : min(n, stop - first);
   }
+  __device__ __forceinline__ bool last() const { return whole > 0 ? whole == 1 && at >= stop : first + t1 >= stop; }
   __device__ __forceinline__ bool next() {  // false: nothing left
-    at = first + t1;
-    first += n;
-    ++item;
-    return at < stop;
+    if (last()) return false;
+    if (whole > 0) {
+      item = --whole ? item + 1 : later;
+    } else {
+      at = first + t1;
+      first += n;
+      ++item;
+    }
+    return true;
   }
 };
 
@@ -131,13 +144,23 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int g = blockIdx.x % a.ngroups, u = blockIdx.x / a.ngroups;
   const int h0 = g * NH;
 
-  // the block's units (all threads)
-  const int total = attn_units_before(a, a.Q * a.rows, ms.tmp), ranges = min(a.ranges, total);
-  if (u >= ranges) return;
+  // the block's items and units (all threads)
   Walk w;
-  w.at = range_begin(total, ranges, u);
-  w.stop = range_begin(total, ranges, u + 1);
-  w.item = attn_item_of(a, w.at, ms.tmp, &w.first);
+  {
+    int* tmp = reinterpret_cast<int*>(ms.info);
+    const int total = attn_units_before(a, a.Q * a.rows, tmp), ranges = min(a.ranges, total);
+    w.whole = a.whole;
+    w.later = 0;
+    w.at = w.stop = w.first = 0;
+    if (u < ranges) {
+      w.at = range_begin(total, ranges, u);
+      w.stop = range_begin(total, ranges, u + 1);
+      w.later = attn_item_of(a, w.at, tmp, &w.first);
+    }
+    w.item = w.whole ? u * w.whole : w.later;
+    __syncthreads();
+  }
+  if (!w.whole && w.at >= w.stop) return;
   const int my_begin = w.at;
 
   if (threadIdx.x == 0) {
@@ -147,17 +170,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(bar(B.full[s][p]), kProducers);
         mbar_init(bar(B.empty[s][p]), 1);
       }
-    for (int i = 0; i < kInfo; ++i) mbar_init(bar(B.info[i]), 1);
+    for (int i = 0; i < kInfo; ++i) {
+      mbar_init(bar(B.info[i]), 1);
+      mbar_init(bar(B.infofree[i]), 1);
+    }
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(B.sfull[i]), 1);
-      mbar_init(bar(B.sfree[i]), 4);
+      mbar_init(bar(B.sfree[i]), kSoft / 32);
       mbar_init(bar(B.done[i]), 1);
     }
-    mbar_init(bar(B.pfull), 4);
+    mbar_init(bar(B.pfull), kSoft / 32);
     mbar_init(bar(B.pempty), 1);
-    mbar_init(bar(B.qfull), kQThreads);
+    mbar_init(bar(B.qfull), kProducers);
     mbar_init(bar(B.qempty), 1);
-    mbar_init(bar(B.oempty), 4);
+    mbar_init(bar(B.oempty), kSoft / 32);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == kMmaWarp) tmem_alloc(smem_u32(&ms.tmem), kTmemCols);
@@ -166,127 +192,177 @@ __global__ void __launch_bounds__(kThreads, 1)
   fence_after();
   const uint32_t tmem = ms.tmem;
 
-  if (warp >= 4 && warp < kMmaWarp) {
-    // ======================= producers =======================
-    // Each warp looks up all 64 tokens (lane l: 2 l, 2 l + 1), so that all
-    // agree on which tiles are passed over; it copies tokens 4 pw + l / 8 + 16 j,
-    // piece l % 8 of each 128-byte line.
+  if (warp == kLookWarp) {
+    // ======================= look-up =======================
+    // Lane l takes tokens 2 l and 2 l + 1, two units at a time.
     const LatentCache& C = a.cache;
-    const int pw = warp - 4;
-    struct Look {      // one unit of the stream
-      int q, end, flags;
-      int slot[2];     // entries (list) or slots
-      int page[2];
+    const char* data = reinterpret_cast<const char*>(C.data);
+    struct Look {
+      int item, q, end, flags;
+      int slot[2], page[2];
     };
-    // stage 1: the unit's entries
-    auto entries = [&](Look& x, bool& more) {
-      if (!more) {
-        x.q = -1;
-        return;
-      }
-      const int k = w.at - w.first;
-      x.q = w.q;
-      x.end = w.end;
-      x.flags = (k == w.t1 - 1 ? 2 : 0) | (w.at + 1 == w.stop ? 4 : 0);
-      const int e0 = k * kTok + 2 * lane;
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        x.slot[i] = -1;
-        if (a.list) {
-          if (e0 + i < a.topk) x.slot[i] = __ldg(a.list + (int64_t)w.item * a.topk + e0 + i);
-        } else {
-          x.slot[i] = e0 + i;
-        }
-      }
-      if (++w.at == w.first + w.t1) {
-        more = w.at < w.stop;
-        if (more) {
-          w.first += w.n;
-          ++w.item;
-          w.open(a);
-        }
-      }
-    };
-    // stage 2: their pages
-    auto pages = [&](Look& x) {
-      if (x.q < 0) return;
-      const int32_t* bt = C.bt + (int64_t)x.q * C.bt_stride;
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        if (x.slot[i] >= x.end) x.slot[i] = -1;
-        x.page[i] = x.slot[i] >= 0 ? __ldg(bt + (x.slot[i] >> C.log2b)) : 0;
-      }
-    };
-    bool more = true;
-    w.open(a);
-    Look x0, x1, x2;
-    entries(x0, more);
-    entries(x1, more);
-    pages(x0);
     int tile = 0;
-    bool ok = true, fresh = true;
-    const char* base = reinterpret_cast<const char*>(C.data) + (lane & 7) * 16;
-    while (x0.q >= 0) {
-      entries(x2, more);
-      pages(x1);
-      // rows and mask of x0
-      int row[2];
-      bool live[2];
+    bool more = true, ok = true, fresh = true;
+    w.open(a);
+    int k = w.t0;
+    while (more && ok) {
+      Look x[2];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        live[i] = x0.slot[i] >= 0;
-        if (live[i] && (x0.page[i] < 0 || x0.page[i] >= C.num_pages)) {
-          if (pw == 0) raise_error(a.err, ERR_PAGE, x0.q, (uint32_t)x0.page[i]);
-          live[i] = false;
+      for (int v = 0; v < 2; ++v) {  // the list's entries
+        x[v].q = -1;
+        if (!more) continue;
+        x[v].item = w.item;
+        x[v].q = w.q;
+        x[v].end = w.end;
+        x[v].flags = k < w.t1 - 1 ? 0 : w.last() ? 6 : 2;
+        const int e0 = k * kTok + 2 * lane;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          x[v].slot[i] = -1;
+          if (a.list) {
+            if (e0 + i < a.topk) x[v].slot[i] = __ldg(a.list + (int64_t)w.item * a.topk + e0 + i);
+          } else {
+            x[v].slot[i] = e0 + i;
+          }
         }
-        row[i] = live[i] ? (x0.page[i] << C.log2b) + (x0.slot[i] & (C.b - 1)) : -1;
+        if (++k == w.t1) {
+          more = w.next();
+          if (more) {
+            w.open(a);
+            k = w.t0;
+          }
+        }
       }
-      const uint32_t even = __ballot_sync(0xffffffffu, live[0]), odd = __ballot_sync(0xffffffffu, live[1]);
-      if (even || odd || (x0.flags & 2)) {  // a tile of which nothing is attended to is passed over
-        const int st = tile % kStages;
-        const uint32_t par = (uint32_t)(tile / kStages) & 1u;
-        const char* src[4];
-        uint32_t dst[4], bytes[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int t = 4 * pw + (lane >> 3) + 16 * j;
-          const int r0 = __shfl_sync(0xffffffffu, row[0], t >> 1), r1 = __shfl_sync(0xffffffffu, row[1], t >> 1);
-          const int r = (t & 1) ? r1 : r0;
-          bytes[j] = r >= 0 ? 16u : 0u;  // 0: filled with zeros, nothing is read
-          src[j] = base + (int64_t)(r >= 0 ? r : 0) * (kW * 2);
-          dst[j] = kv_at + st * kStageBytes + t * 128 + (((lane & 7) ^ (t & 7)) << 4);
+      for (int v = 0; v < 2; ++v)  // their pages
+        if (x[v].q >= 0) {
+          const int32_t* bt = C.bt + (int64_t)x[v].q * C.bt_stride;
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            if (x[v].slot[i] >= x[v].end) x[v].slot[i] = -1;
+            x[v].page[i] = x[v].slot[i] >= 0 ? __ldg(bt + (x[v].slot[i] >> C.log2b)) : 0;
+          }
         }
 #pragma unroll
-        for (int j = 0; j < kParts; ++j) {
-          const int p = j == 0 ? 4 : j - 1;  // kr first: S starts with it
-          ok = wait_warp(bar(B.empty[st][p]), par ^ 1u, ctl);
-          if (!ok) break;
-          if (j == 0 && pw == 0 && lane == 0) {
-            // the second product of tile - 4, the slot's last user, is done: tile - 2 took its stage
-            Info& f = ms.info[tile % kInfo];
-            f.even = even;
-            f.odd = odd;
-            f.flags = x0.flags | (fresh ? 1 : 0);
-            mbar_arrive(bar(B.info[tile % kInfo]));
-          }
+      for (int v = 0; v < 2; ++v) {  // cache rows and mask
+        if (x[v].q < 0 || !ok) continue;
+        int row[2];
 #pragma unroll
-          for (int b = 0; b < (p == 4 ? 1 : 2); ++b) {
-            const int blk = p == 4 ? 8 : 2 * p + b;
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst[i] + blk * kBlk),
-                           "l"(src[i] + blk * 128), "r"(bytes[i])
-                           : "memory");
+        for (int i = 0; i < 2; ++i) {
+          bool live = x[v].slot[i] >= 0;
+          if (live && (x[v].page[i] < 0 || x[v].page[i] >= C.num_pages)) {
+            raise_error(a.err, ERR_PAGE, x[v].q, (uint32_t)x[v].page[i]);
+            live = false;
           }
-          // arrives when this thread's copies so far have landed
-          asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar(B.full[st][p])) : "memory");
+          row[i] = live ? (x[v].page[i] << C.log2b) + (x[v].slot[i] & (C.b - 1)) : -1;
+          if (live) {
+#pragma unroll
+            for (int c = 0; c < kBlocks; ++c)  // (one bulk prefetch a row instead took 40 cycles a row to issue)
+              asm volatile("prefetch.global.L2 [%0];" ::"l"(data + (int64_t)row[i] * (kW * 2) + c * 128) : "memory");
+          }
         }
-        if (!ok) break;
-        fresh = x0.flags & 2;
+        const uint32_t even = __ballot_sync(0xffffffffu, row[0] >= 0), odd = __ballot_sync(0xffffffffu, row[1] >= 0);
+        if (!even && !odd && !(x[v].flags & 2)) continue;  // nothing of the tile is attended to
+        const int at = tile % kInfo;
+        if (tile >= kInfo) ok = wait_warp(bar(B.infofree[at]), (uint32_t)(tile / kInfo - 1) & 1u, ctl);
+        if (!ok) continue;
+        Info& f = ms.info[at];
+        f.row[2 * lane] = row[0];
+        f.row[2 * lane + 1] = row[1];
+        if (lane == 0) {
+          f.even = even;
+          f.odd = odd;
+          f.flags = x[v].flags | (fresh ? 1 : 0);
+          f.item = x[v].item;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(B.info[at]));
+        fresh = x[v].flags & 2;
         ++tile;
       }
-      x0 = x1;
-      x1 = x2;
+    }
+  } else if (warp >= kCopyWarp && warp < kMmaWarp) {
+    // ======================= producers =======================
+    // This thread copies piece lane % 8 of each 128-byte line of tokens row0 + 16 j.
+    const int pw = warp - kCopyWarp;
+    const char* data = reinterpret_cast<const char*>(a.cache.data);
+    // this thread's 4 rows' copies of one 64-column block
+    const int piece = lane & 7, row0 = 4 * pw + (lane >> 3);
+    auto copy = [&](uint32_t dst, const char* src, uint32_t bytes) {
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+    };
+    // arrives when this thread's copies so far have landed
+    auto landed = [&](uint64_t& b) {
+      asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar(b)) : "memory");
+    };
+    auto queries = [&](int item) {
+      const char* ql = reinterpret_cast<const char*>(a.ql) + (int64_t)item * a.ql_tok * 2;
+      const char* qr = reinterpret_cast<const char*>(a.qr) + (int64_t)item * a.qr_tok * 2;
+#pragma unroll 1
+      for (int h = row0; h < NH; h += 16) {
+        const bool live = h0 + h < H;  // else zeros
+        const char* l = ql + (int64_t)(live ? h0 + h : 0) * a.ql_head * 2 + piece * 16;
+        const char* r = qr + (int64_t)(live ? h0 + h : 0) * a.qr_head * 2 + piece * 16;
+        const uint32_t dst = q_at + h * 128 + ((piece ^ (h & 7)) << 4);
+        if (a.q_vec) {
+#pragma unroll
+          for (int blk = 0; blk < kBlocks; ++blk) copy(dst + blk * NH * 128, blk < 8 ? l + blk * 128 : r, live ? 16u : 0u);
+        } else {  // queries that do not lie on 16 bytes
+#pragma unroll 1
+          for (int blk = 0; blk < kBlocks; ++blk) {
+            const uint16_t* e = reinterpret_cast<const uint16_t*>(blk < 8 ? l + blk * 128 : r);
+            uint32_t v[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) v[k] = live ? (uint32_t)e[2 * k] | (uint32_t)e[2 * k + 1] << 16 : 0u;
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + blk * NH * 128), "r"(v[0]), "r"(v[1]),
+                         "r"(v[2]), "r"(v[3])
+                         : "memory");
+          }
+        }
+      }
+      landed(B.qfull);
+    };
+    queries(w.item);
+    int seg = 0, flags = 0;
+    for (int tile = 0; !(flags & 4); ++tile) {
+      const int st = tile % kStages;
+      const uint32_t par = (uint32_t)(tile / kStages) & 1u ^ 1u;
+      if (!wait_warp2(bar(B.info[tile % kInfo]), (uint32_t)(tile / kInfo) & 1u, bar(B.empty[st][4]), par, ctl)) break;
+      const Info& f = ms.info[tile % kInfo];
+      flags = f.flags;
+      const int item = f.item;
+      const char* src[4];
+      uint32_t dst[4], bytes[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int t = row0 + 16 * j, r = f.row[t];
+        bytes[j] = r >= 0 ? 16u : 0u;  // 0: filled with zeros, nothing is read
+        src[j] = data + piece * 16 + (int64_t)(r >= 0 ? r : 0) * (kW * 2);
+        dst[j] = kv_at + st * kStageBytes + t * 128 + ((piece ^ (t & 7)) << 4);
+      }
+      auto block = [&](int blk) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) copy(dst[i] + blk * kBlk, src[i] + blk * 128, bytes[i]);
+      };
+      block(8);  // kr first: S starts with it
+      landed(B.full[st][4]);
+      bool ok = true;
+#pragma unroll
+      for (int p = 0; p < 4; ++p) {
+        ok = ok && wait_warp(bar(B.empty[st][p]), par, ctl);
+        if (!ok) break;
+        block(2 * p);
+        block(2 * p + 1);
+        landed(B.full[st][p]);
+      }
+      if (!ok) break;
+      if ((flags & 1) && seg > 0) {
+        // (behind the tile's copies: those wait for the second product of two tiles ago, the queries' place for
+        // the first product of the last, which comes later)
+        if (!wait_warp(bar(B.qempty), (uint32_t)(seg - 1) & 1u, ctl)) break;
+        queries(item);
+      }
+      if (flags & 2) ++seg;
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
   } else if (warp == kMmaWarp) {
@@ -295,43 +371,44 @@ __global__ void __launch_bounds__(kThreads, 1)
     // products are issued by two warps, each waiting for its own operands:
     // one warp that polled for both spent more time polling than the MMAs take.
     const uint32_t id_s = idesc_bf16(64, kTok, 0, 0);
-    const uint64_t a2 = (uint64_t)(NH * 128 >> 4), b2 = kBlk >> 4;
+    const uint64_t a1 = (uint64_t)(NH * 128 >> 4), b1 = kBlk >> 4;  // a 64-column block further
     int seg = 0, flags = 0;
-    bool ok = true;
-    for (int tile = 0; ok && !(flags & 4); ++tile) {
+    for (int tile = 0; !(flags & 4); ++tile) {
       const int st = tile % kStages;
-      ok = wait_warp(bar(B.info[tile % kInfo]), (uint32_t)(tile / kInfo) & 1u, ctl);
-      if (!ok) break;
+      const uint32_t par = (uint32_t)(tile / kStages) & 1u;
+      // S's buffer is that of two tiles ago (an untouched barrier has "completed" parity 1)
+      if (!wait_warp2(bar(B.info[tile % kInfo]), (uint32_t)(tile / kInfo) & 1u, bar(B.sfree[tile & 1]),
+                      (uint32_t)(tile >> 1) & 1u ^ 1u, ctl))
+        break;
       flags = __shfl_sync(0xffffffffu, ms.info[tile % kInfo].flags, 0);
-      if (flags & 1) ok = wait_warp(bar(B.qfull), (uint32_t)seg & 1u, ctl);
-      // S's buffer is that of two tiles ago
-      if (ok && tile >= 2) ok = wait_warp(bar(B.sfree[tile & 1]), (uint32_t)((tile >> 1) - 1) & 1u, ctl);
+      if ((flags & 1) && !wait_warp(bar(B.qfull), (uint32_t)seg & 1u, ctl)) break;
       const uint32_t d = tmem + kSCol + (uint32_t)(tile & 1) * kTok;
+      const uint64_t ad = sw128_desc(q_at, 16, 1024), bd = sw128_desc(kv_at + st * kStageBytes, 16, 1024);
+      auto block = [&](int blk) {
 #pragma unroll
-      for (int j = 0; j < kParts; ++j) {
-        const int p = j == 0 ? 4 : j - 1;
-        ok = ok && wait_warp(bar(B.full[st][p]), (uint32_t)(tile / kStages) & 1u, ctl);
-        if (!ok) break;
-        fence_async_smem();  // the copies are generic-proxy writes, the MMAs read through the async proxy
-        fence_after();
-        const uint64_t ad = sw128_desc(q_at + 2 * p * NH * 128, 16, 1024);
-        const uint64_t bd = sw128_desc(kv_at + st * kStageBytes + 2 * p * kBlk, 16, 1024);
-        if (elect()) {
+        for (int kk = 0; kk < 4; ++kk)
+          mma_f16(d, ad + blk * a1 + 2 * kk, bd + blk * b1 + 2 * kk, id_s, blk < 8 || kk > 0 ? 1u : 0u);
+      };
+      // kr and the first half of c, then the second half
+      if (!wait_warp2(bar(B.full[st][4]), par, bar(B.full[st][1]), par, ctl)) break;  // (part 0 lands before part 1)
+      fence_async_smem();  // the copies are generic-proxy writes, the MMAs read through the async proxy
+      fence_after();
+      if (elect()) {
+        block(8);
+        commit(bar(B.empty[st][4]));
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk) mma_f16(d, ad + 2 * kk, bd + 2 * kk, id_s, j > 0 || kk > 0 ? 1u : 0u);
-          if (p == 4) {
-            commit(bar(B.empty[st][4]));
-          } else {
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk) mma_f16(d, ad + a2 + 2 * kk, bd + b2 + 2 * kk, id_s, 1u);
-          }
-          if (j == kParts - 1) {
-            commit(bar(B.sfull[tile & 1]));
-            if (flags & 2) commit(bar(B.qempty));
-          }
-        }
-        __syncwarp();
+        for (int blk = 0; blk < 4; ++blk) block(blk);
       }
+      __syncwarp();
+      if (!wait_warp2(bar(B.full[st][2]), par, bar(B.full[st][3]), par, ctl)) break;
+      fence_async_smem();
+      if (elect()) {
+#pragma unroll
+        for (int blk = 4; blk < 8; ++blk) block(blk);
+        commit(bar(B.sfull[tile & 1]));
+        if (flags & 2) commit(bar(B.qempty));
+      }
+      __syncwarp();
       if (flags & 2) ++seg;
     }
     // every MMA is complete before TMEM is given back
@@ -344,9 +421,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     int seg = 0, flags = 0;
     for (int tile = 0; !(flags & 4); ++tile) {
       const int st = tile % kStages;
-      if (!wait_warp(bar(B.info[tile % kInfo]), (uint32_t)(tile / kInfo) & 1u, ctl)) break;
+      if (!wait_warp2(bar(B.info[tile % kInfo]), (uint32_t)(tile / kInfo) & 1u, bar(B.pfull), (uint32_t)tile & 1u, ctl))
+        break;
       flags = __shfl_sync(0xffffffffu, ms.info[tile % kInfo].flags, 0);
-      if (!wait_warp(bar(B.pfull), (uint32_t)tile & 1u, ctl)) break;
       if ((flags & 1) && seg > 0 && !wait_warp(bar(B.oempty), (uint32_t)(seg - 1) & 1u, ctl)) break;
       fence_after();
       const uint64_t ad = sw128_desc(kv_at + st * kStageBytes, kBlk, 1024), bd = sw128_desc(p_at, 16, 1024);
@@ -361,6 +438,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           commit(bar(B.empty[st][mb]));
         }
         commit(bar(B.pempty));
+        commit(bar(B.infofree[tile % kInfo]));
       }
       __syncwarp();
       if (flags & 2) ++seg;
@@ -368,50 +446,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (elect()) commit(bar(B.done[1]));
     __syncwarp();
     drain(bar(B.done[1]), 0);
-  } else if (warp > kMmaWarp + 1) {
-    // ======================= Q tiles =======================
-    const int t = threadIdx.x - (kMmaWarp + 2) * 32;
-    bool more = true;
-    for (int seg = 0; more; ++seg) {
-      w.open(a);
-      if (seg > 0 && !wait_warp(bar(B.qempty), (uint32_t)(seg - 1) & 1u, ctl)) break;
-      const char* ql = reinterpret_cast<const char*>(a.ql) + (int64_t)w.item * a.ql_tok * 2;
-      const char* qr = reinterpret_cast<const char*>(a.qr) + (int64_t)w.item * a.qr_tok * 2;
-      // 16-byte pieces: 72 a head, piece c of head h at block c / 8, row h, place (c % 8) ^ (h % 8)
-      for (int i = t; i < NH * (kW / 8); i += kQThreads) {
-        const int h = i / (kW / 8), c = i - h * (kW / 8);
-        const uint32_t dst = q_at + (uint32_t)((c >> 3) * NH * 128 + h * 128 + (((c & 7) ^ (h & 7)) << 4));
-        if (h0 + h < H) {
-          const char* src = c < kDC / 8 ? ql + (int64_t)(h0 + h) * a.ql_head * 2 + c * 16
-                                        : qr + (int64_t)(h0 + h) * a.qr_head * 2 + (c - kDC / 8) * 16;
-          if (a.q_vec) {
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-          } else {  // queries that do not lie on 16 bytes
-            const uint16_t* e = reinterpret_cast<const uint16_t*>(src);
-            uint32_t v[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) v[k] = (uint32_t)e[2 * k] | (uint32_t)e[2 * k + 1] << 16;
-            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(v[0]), "r"(v[1]), "r"(v[2]),
-                         "r"(v[3])
-                         : "memory");
-          }
-        } else {
-          asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(dst), "r"(0) : "memory");
-        }
-      }
-      asm volatile("cp.async.wait_all;" ::: "memory");
-      fence_async_smem();
-      mbar_arrive(bar(B.qfull));
-      more = w.next();
-    }
   } else {
     // ======================= softmax and output =======================
-    const int hA = 16 * warp + (lane >> 2);  // this thread's heads: hA, hA + 8
-    const uint32_t lanes = (uint32_t)(warp * 32) << 16;
+    const int quarter = warp & 3, half = warp >> 2;
+    const int hA = 16 * quarter + (lane >> 2);  // this thread's heads: hA, hA + 8
+    const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
+    const uint32_t s_at = tmem + lanes + kSCol + (uint32_t)half * 32;
     const uint32_t prow = p_at + (uint32_t)hA * 128 + (uint32_t)(lane & 3) * 4;
     const int sw = hA & 7;  // (hA + 8) & 7 is the same
-    const bool mine = 16 * warp < NH;
-    int tile = 0, seg = 0;
+    const bool mine = 16 * quarter < NH;
+    // the two token halves' maxima, then sums, where the weights lie (while no product reads those)
+    float(*halves)[kTcHeads] = reinterpret_cast<float(*)[kTcHeads]>(p_sm);
+    int tile = 0;
     bool run = true;
     while (run) {
       w.open(a);
@@ -421,70 +467,96 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool alive = true;
       do {
         // ---- scores of the tile ----
-        bool ok = wait_warp(bar(B.info[tile % kInfo]), (uint32_t)(tile / kInfo) & 1u, ctl);
-        ok = ok && wait_warp(bar(B.sfull[tile & 1]), (uint32_t)(tile >> 1) & 1u, ctl);
-        uint32_t s[32];
-        uint32_t even = 0, odd = 0;
+        bool ok = wait_warp2(bar(B.info[tile % kInfo]), (uint32_t)(tile / kInfo) & 1u, bar(B.sfull[tile & 1]),
+                             (uint32_t)(tile >> 1) & 1u, ctl);
+        uint32_t s[16], p[8];
         flags = 0;
-        float t0 = -INFINITY, t1 = -INFINITY;
         if (ok) {
-          even = ms.info[tile % kInfo].even;
-          odd = ms.info[tile % kInfo].odd;
           flags = ms.info[tile % kInfo].flags;
-        }
-        if (ok && mine) {
-          fence_after();
-          tmem_ld_16x256b_x8(tmem + lanes + kSCol + (uint32_t)(tile & 1) * kTok, s);
-          tmem_wait_ld();
-          fence_before();
-        }
-        __syncwarp();
-        if (ok && lane == 0) mbar_arrive(bar(B.sfree[tile & 1]));
-        if (ok && mine) {
-          if ((even & odd) != 0xffffffffu) {
-            // columns 8 n + 2 (lane % 4) and the next: bit 4 n + lane % 4 of the two
-            const uint32_t ev = even >> (lane & 3), od = odd >> (lane & 3);
+          const uint32_t even = ms.info[tile % kInfo].even, odd = ms.info[tile % kInfo].odd;
+          if (mine) {
+            fence_after();
+            tmem_ld_16x256b_x4(s_at + (uint32_t)(tile & 1) * kTok, s);
+            tmem_wait_ld();
+            fence_before();
+            if ((even & odd) != 0xffffffffu) {
+              // columns 32 half + 8 n + 2 (lane % 4) and the next: bit 16 half + 4 n + lane % 4 of the two
+              const uint32_t ev = even >> (16 * half + (lane & 3)), od = odd >> (16 * half + (lane & 3));
 #pragma unroll
-            for (int n = 0; n < 8; ++n) {
-              if (!(ev >> (4 * n) & 1)) s[4 * n] = s[4 * n + 2] = 0xff800000u;
-              if (!(od >> (4 * n) & 1)) s[4 * n + 1] = s[4 * n + 3] = 0xff800000u;
+              for (int n = 0; n < 4; ++n) {
+                if (!(ev >> (4 * n) & 1)) s[4 * n] = s[4 * n + 2] = 0xff800000u;
+                if (!(od >> (4 * n) & 1)) s[4 * n + 1] = s[4 * n + 3] = 0xff800000u;
+              }
             }
           }
-#pragma unroll
-          for (int n = 0; n < 8; ++n) {
-            t0 = fmaxf(t0, fmaxf(__uint_as_float(s[4 * n]), __uint_as_float(s[4 * n + 1])));
-            t1 = fmaxf(t1, fmaxf(__uint_as_float(s[4 * n + 2]), __uint_as_float(s[4 * n + 3])));
-          }
-          t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, 1));
-          t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, 1));
-          t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, 2)) * a.scale_log2;
-          t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, 2)) * a.scale_log2;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(B.sfree[tile & 1]));
         }
-        // ---- the reference moves where a row outgrew it ----
-        const bool grow = mine && (t0 > m0 + kLazy || t1 > m1 + kLazy);
-        if (bar_or(1, 128, grow || !ok)) {
+        // ---- weights by the reference that there is; where a row outgrew it (the first tile always), it moves
+        // and they are taken again ----
+        float d0, d1;
+        for (int pass = 0;; ++pass) {
+          bool grow = false;
+          d0 = d1 = 0.f;
+          if (ok && mine) {
+            const float r0 = m0 == -INFINITY ? 0.f : m0, r1 = m1 == -INFINITY ? 0.f : m1;
+            float x0 = -INFINITY, x1 = -INFINITY;
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {
+              const float s0 = fmaf(__uint_as_float(s[4 * n]), a.scale_log2, -r0);
+              const float s1 = fmaf(__uint_as_float(s[4 * n + 1]), a.scale_log2, -r0);
+              const float s2 = fmaf(__uint_as_float(s[4 * n + 2]), a.scale_log2, -r1);
+              const float s3 = fmaf(__uint_as_float(s[4 * n + 3]), a.scale_log2, -r1);
+              x0 = fmaxf(x0, fmaxf(s0, s1));
+              x1 = fmaxf(x1, fmaxf(s2, s3));
+              const float p0 = ex2(s0), p1 = ex2(s1), p2 = ex2(s2), p3 = ex2(s3);
+              d0 += p0 + p1;
+              d1 += p2 + p3;
+              p[2 * n] = pack_bf16(p0, p1);
+              p[2 * n + 1] = pack_bf16(p2, p3);
+            }
+            grow = x0 > (m0 == -INFINITY ? -INFINITY : kLazy) || x1 > (m1 == -INFINITY ? -INFINITY : kLazy);
+          }
+          if (pass || !bar_or(1, kSoft, grow || !ok)) break;
           // (the second product of the tile before has read the weights and O is whole)
           if (ok && tile > 0) ok = wait_warp(bar(B.pempty), (uint32_t)(tile - 1) & 1u, ctl);
+          float t0 = -INFINITY, t1 = -INFINITY;
+          if (ok && mine) {
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {
+              t0 = fmaxf(t0, fmaxf(__uint_as_float(s[4 * n]), __uint_as_float(s[4 * n + 1])));
+              t1 = fmaxf(t1, fmaxf(__uint_as_float(s[4 * n + 2]), __uint_as_float(s[4 * n + 3])));
+            }
+#pragma unroll
+            for (int d = 1; d <= 2; d <<= 1) {
+              t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, d));
+              t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, d));
+            }
+            if ((lane & 3) == 0) {
+              halves[half][hA] = t0;
+              halves[half][hA + 8] = t1;
+            }
+          }
+          alive = !bar_or(1, kSoft, !ok);
+          if (!alive) break;
           if (mine) {
-            const float n0 = fmaxf(m0, t0), n1 = fmaxf(m1, t1);
+            const float n0 = fmaxf(m0, fmaxf(t0, halves[half ^ 1][hA]) * a.scale_log2);
+            const float n1 = fmaxf(m1, fmaxf(t1, halves[half ^ 1][hA + 8]) * a.scale_log2);
             const float f0 = n0 == -INFINITY ? 1.f : ex2(m0 - n0), f1 = n1 == -INFINITY ? 1.f : ex2(m1 - n1);
             l0 *= f0;
             l1 *= f1;
             m0 = n0;
             m1 = n1;
-            if ((lane & 3) == 0) {
+            if (half == 0 && (lane & 3) == 0) {
               ms.fac[hA] = f0;
               ms.fac[hA + 8] = f1;
             }
           }
-          if (bar_or(1, 128, !ok)) {
-            alive = false;
-            break;
-          }
+          bar_sync(1, kSoft);  // the factors are there, the halves' maxima have been read
           if (!(flags & 1)) {
             fence_after();
 #pragma unroll 1
-            for (int c = 0; c < 4 * NH; c += 16) {
+            for (int c = 2 * half * NH; c < 2 * (half + 1) * NH; c += 16) {
               uint32_t o[16];
               tmem_ld16(tmem + lanes + (uint32_t)c, o);
               tmem_wait_ld();
@@ -500,31 +572,19 @@ __global__ void __launch_bounds__(kThreads, 1)
               tmem_st16(tmem + lanes + (uint32_t)c, o);
             }
             tmem_wait_st();
-          }
-          bar_sync(1, 128);  // the factors have been read
-        }
-        // ---- weights ----
-        if (mine) {
-          const float r0 = m0 == -INFINITY ? 0.f : m0, r1 = m1 == -INFINITY ? 0.f : m1;
-#pragma unroll
-          for (int n = 0; n < 8; ++n) {
-            const float p0 = ex2(fmaf(__uint_as_float(s[4 * n]), a.scale_log2, -r0));
-            const float p1 = ex2(fmaf(__uint_as_float(s[4 * n + 1]), a.scale_log2, -r0));
-            const float p2 = ex2(fmaf(__uint_as_float(s[4 * n + 2]), a.scale_log2, -r1));
-            const float p3 = ex2(fmaf(__uint_as_float(s[4 * n + 3]), a.scale_log2, -r1));
-            l0 += p0 + p1;
-            l1 += p2 + p3;
-            s[2 * n] = pack_bf16(p0, p1);
-            s[2 * n + 1] = pack_bf16(p2, p3);
+            bar_sync(1, kSoft);  // the factors have been read
           }
         }
+        if (!alive) break;
+        l0 += d0;
+        l1 += d1;
         ok = tile == 0 || wait_warp(bar(B.pempty), (uint32_t)(tile - 1) & 1u, ctl);
         if (ok && mine) {
 #pragma unroll
-          for (int n = 0; n < 8; ++n) {
-            const uint32_t at = prow + (uint32_t)((n ^ sw) << 4);
-            asm volatile("st.shared.b32 [%0], %1;" ::"r"(at), "r"(s[2 * n]) : "memory");
-            asm volatile("st.shared.b32 [%0], %1;" ::"r"(at + 1024), "r"(s[2 * n + 1]) : "memory");
+          for (int n = 0; n < 4; ++n) {
+            const uint32_t at = prow + (uint32_t)(((4 * half + n) ^ sw) << 4);
+            asm volatile("st.shared.b32 [%0], %1;" ::"r"(at), "r"(p[2 * n]) : "memory");
+            asm volatile("st.shared.b32 [%0], %1;" ::"r"(at + 1024), "r"(p[2 * n + 1]) : "memory");
           }
           fence_async_smem();
         }
@@ -538,17 +598,23 @@ __global__ void __launch_bounds__(kThreads, 1)
 
       // ---- the item's end ----
       bool ok = wait_warp(bar(B.pempty), (uint32_t)(tile - 1) & 1u, ctl);
-      l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
-      l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
-      l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
-      l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
+#pragma unroll
+      for (int d = 1; d <= 2; d <<= 1) {
+        l0 += __shfl_xor_sync(0xffffffffu, l0, d);
+        l1 += __shfl_xor_sync(0xffffffffu, l1, d);
+      }
+      if (half == 1 && mine && (lane & 3) == 0) {
+        halves[1][hA] = l0;
+        halves[1][hA + 8] = l1;
+      }
+      if (bar_or(1, kSoft, !ok)) break;
       const bool whole = w.t0 == 0 && w.t1 == w.n;
       const int64_t part = (int64_t)blockIdx.x * 2 + (w.first <= my_begin ? 0 : 1);
-      if (mine && (lane & 3) == 0) {
+      if (half == 0 && mine && (lane & 3) == 0) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const int h = hA + 8 * i;
-          const float m = i ? m1 : m0, l = i ? l1 : l0;
+          const float m = i ? m1 : m0, l = (i ? l1 : l0) + halves[1][h];
           if (whole) {
             ms.fac[h] = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
             if (a.lse && h0 + h < H)
@@ -558,40 +624,46 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      if (bar_or(1, 128, !ok)) break;
+      bar_sync(1, kSoft);
       fence_after();
       const int nh = min(NH, H - h0);
-#pragma unroll 1
-      for (int mb = 0; mb < 4; ++mb) {
-        const int d = mb * 128 + warp * 32 + lane;
-#pragma unroll 1
-        for (int c = 0; c < NH; c += 16) {
-          uint32_t o[16];
-          tmem_ld16(tmem + lanes + (uint32_t)(mb * NH + c), o);
-          tmem_wait_ld();
-          if (whole) {
-            __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(a.out) +
-                                 ((int64_t)w.item * H + h0 + c + (lane & 1)) * kDC + (d & ~1);
+      // 16 heads x 128 columns at a time, the next ones' load in flight; the two halves take 256 columns each
+      const int steps = 2 * (NH / 16);
+      const uint32_t o_at = tmem + lanes + (uint32_t)(2 * half * NH);
+      uint32_t o[2][16];
+      tmem_ld16(o_at, o[0]);
+      auto put = [&](int i, const uint32_t (&o)[16]) {
+        const int mb = i * 16 / NH, c = i * 16 - mb * NH, d = (2 * half + mb) * 128 + quarter * 32 + lane;
+        if (whole) {
+          __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(a.out) +
+                               ((int64_t)w.item * H + h0 + c + (lane & 1)) * kDC + (d & ~1);
 #pragma unroll
-            for (int i = 0; i < 16; i += 2) {
-              // neighbouring lanes trade halves: each gets two columns of one head
-              const float x = __uint_as_float(o[i]) * ms.fac[c + i], y = __uint_as_float(o[i + 1]) * ms.fac[c + i + 1];
-              const float z = __shfl_xor_sync(0xffffffffu, (lane & 1) ? x : y, 1);
-              if (c + i + (lane & 1) < nh)
-                *reinterpret_cast<uint32_t*>(out + (int64_t)i * kDC) = (lane & 1) ? pack_bf16(z, y) : pack_bf16(x, z);
-            }
-          } else {
-            float* out = a.part + (part * NH + c) * kDC + d;
-#pragma unroll
-            for (int i = 0; i < 16; ++i) out[(int64_t)i * kDC] = __uint_as_float(o[i]);
+          for (int k = 0; k < 16; k += 2) {
+            // neighbouring lanes trade halves: each gets two columns of one head
+            const float x = __uint_as_float(o[k]) * ms.fac[c + k], y = __uint_as_float(o[k + 1]) * ms.fac[c + k + 1];
+            const float z = __shfl_xor_sync(0xffffffffu, (lane & 1) ? x : y, 1);
+            if (c + k + (lane & 1) < nh)
+              *reinterpret_cast<uint32_t*>(out + (int64_t)k * kDC) = (lane & 1) ? pack_bf16(z, y) : pack_bf16(x, z);
           }
+        } else {
+          float* out = a.part + (part * NH + c) * kDC + d;
+#pragma unroll
+          for (int k = 0; k < 16; ++k) out[k * kDC] = __uint_as_float(o[k]);
         }
+      };
+#pragma unroll 1
+      for (int i = 0; i < steps; i += 2) {  // steps is even
+        tmem_wait_ld();
+        tmem_ld16(o_at + (uint32_t)(i + 1) * 16, o[1]);
+        put(i, o[0]);
+        tmem_wait_ld();
+        if (i + 2 < steps) tmem_ld16(o_at + (uint32_t)(i + 2) * 16, o[0]);
+        put(i + 1, o[1]);
       }
       fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(B.oempty));
-      bar_sync(1, 128);  // the factors have been read
-      ++seg;
+      bar_sync(1, kSoft);  // the factors have been read
       run = w.next();
     }
   }

@@ -312,17 +312,19 @@ spin_status spin_latent_attention(spin_latent lt, int rows, const void* cache, i
     a.ngroups = (a.H + group - 1) / group;
     const int64_t n = a.list ? a.topk : a.max_slots;
     a.ranges = (int)std::min<int64_t>(std::max(1, blocks / a.ngroups), (int64_t)a.Q * rows * ((n + tile - 1) / tile));
+    a.whole = 0;
   };
   cudaError_t e;
   if (attn_tc_supported(a, bf16)) {
     const int groups = (a.H + kTcHeads - 1) / kTcHeads;
     plan(kTcTile, ((a.H + groups - 1) / groups + 15) / 16 * 16, std::min(lt->sms, kTcBlocks));
+    if (a.list) a.whole = a.Q * rows / a.ranges;
     e = launch_attn_tc(a, (cudaStream_t)stream);
   } else {
     plan(kSimtTile, kSimtHeads, std::min(2 * lt->sms, kSimtBlocks));
     e = launch_attn_simt(a, bf16, (cudaStream_t)stream);
   }
-  if (e == cudaSuccess) e = launch_attn_combine(a, bf16, (cudaStream_t)stream);
+  if (e == cudaSuccess && a.whole * a.ranges < a.Q * rows) e = launch_attn_combine(a, bf16, (cudaStream_t)stream);
   return cuda_status(e);
 }
 

@@ -95,7 +95,9 @@ cudaError_t launch_append(const AppendArgs& a, int bf16, cudaStream_t s);
 // unnormalised output, in fp32 -- in one of its two slots of the workspace
 // (slot 0: the item that holds the block's first unit, slot 1: the item that
 // runs on past its last), and the combine kernel joins the shares in block
-// order, so the result does not depend on timing.
+// order, so the result does not depend on timing.  Lists make all items
+// equally long: there each block takes `whole` items whole before its range
+// of the other items' units, which halves what is left as shares.
 // ---------------------------------------------------------------------------
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -118,6 +120,7 @@ struct AttnArgs {
   int group;                 // heads of a block
   int ngroups;               // ceil(H / group)
   int ranges;                // blocks per head group, at most
+  int whole;                 // items that each block takes whole (lists only)
   float* part;               // [ngroups * ranges * 2][group][dc] unnormalised outputs
   float2* part_ml;           // [ngroups * ranges * 2][group] (maximum in log2 units, sum)
 };
@@ -133,11 +136,11 @@ __device__ __forceinline__ int attn_tiles(const AttnArgs& a, int end) {
   return n > 0 ? (n + a.tile - 1) / a.tile : 1;
 }
 
-// Units before `item` (Q * rows: all of them), summed by all threads of the
-// block; tmp: 35 ints of shared memory.  The host has checked that all units
+// Units of the items that are not taken whole, before `item` (Q * rows: all
+// of them), summed by all threads of the block; tmp: 35 ints of shared memory.  The host has checked that all units
 // together fit 31 bits.
 __device__ __forceinline__ int attn_units_before(const AttnArgs& a, int item, int* tmp) {
-  if (a.list) return item * ((a.topk + a.tile - 1) / a.tile);
+  if (a.list) return (item - a.whole * a.ranges) * ((a.topk + a.tile - 1) / a.tile);
   int sum = 0;
   for (int i = threadIdx.x; i < item; i += blockDim.x) sum += attn_tiles(a, attn_end(a, i / a.rows, i % a.rows));
 #pragma unroll
@@ -156,7 +159,7 @@ __device__ __forceinline__ int attn_item_of(const AttnArgs& a, int g, int* tmp, 
   if (a.list) {
     const int per = (a.topk + a.tile - 1) / a.tile;
     *first = g / per * per;
-    return g / per;
+    return a.whole * a.ranges + g / per;
   }
   const int items = a.Q * a.rows;
   int carry = 0;

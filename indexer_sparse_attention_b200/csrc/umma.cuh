@@ -55,18 +55,6 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
       : "memory");
   return ok != 0;
 }
-// Without the wait that try_wait may make: for a role that polls several.
-__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
 __device__ __forceinline__ uint64_t gtimer() {
   uint64_t t;
   asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
@@ -102,8 +90,11 @@ __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, Ctl c) {
 __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, Ctl c) {
   return __all_sync(0xffffffffu, wait(bar, parity, c));
 }
-__device__ __forceinline__ bool test_warp(uint32_t bar, uint32_t parity) {
-  return __all_sync(0xffffffffu, mbar_test(bar, parity));
+// Two barriers at once (each check costs the latency of shared memory and a
+// vote): even lanes wait for the first, odd lanes for the second.
+__device__ __forceinline__ bool wait_warp2(uint32_t bar0, uint32_t parity0, uint32_t bar1, uint32_t parity1, Ctl c) {
+  const bool odd = threadIdx.x & 1;
+  return __all_sync(0xffffffffu, wait(odd ? bar1 : bar0, odd ? parity1 : parity0, c));
 }
 // One lane of a converged warp.  tcgen05.mma and its descriptors live on the
 // uniform datapath: issued by the elected lane of a warp whose control flow
@@ -214,16 +205,14 @@ __device__ __forceinline__ void tmem_alloc(uint32_t slot, uint32_t cols) {
 __device__ __forceinline__ void tmem_dealloc(uint32_t base, uint32_t cols) {
   asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(base), "r"(cols) : "memory");
 }
-// 16 lanes x 64 columns: thread t gets, of columns 8 n + 2 (t % 4) and the
+// 16 lanes x 32 columns: thread t gets, of columns 8 n + 2 (t % 4) and the
 // next, lane t / 4 in r[4 n], r[4 n + 1] and lane t / 4 + 8 in r[4 n + 2], r[4 n + 3].
-__device__ __forceinline__ void tmem_ld_16x256b_x8(uint32_t addr, uint32_t (&r)[32]) {
+__device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t addr, uint32_t (&r)[16]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-      "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15}, [%16];"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
-        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
-        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(addr));
 }
 // 32 lanes x 16 or 32 columns: a lane per thread.
