@@ -422,7 +422,7 @@ cudaError_t launch_attn_simt(const AttnArgs& a, int bf16, cudaStream_t s) {
 cudaError_t launch_attn_combine(const AttnArgs& a, int bf16, cudaStream_t s) {
   // an item's shares, at the even lengths of lists: a few for many items, else many
   const int items = a.Q * a.rows - a.whole * a.ranges;
-  const bool many = a.ranges > 3 * items;
+  const bool many = a.ranges > 12 * items;
   const int per = many ? 1 : kJoinWarps;
   auto kernel = many ? (bf16 ? k_attn_combine<__nv_bfloat16, kJoinWarps> : k_attn_combine<float, kJoinWarps>)
                      : (bf16 ? k_attn_combine<__nv_bfloat16, 1> : k_attn_combine<float, 1>);

@@ -91,8 +91,9 @@ struct Misc {
   int abort_flag;
 };
 
+constexpr int kPBytes = kTcHeads * 128;  // the weights, at an item's end a place to transpose its output
 __host__ __device__ constexpr uint32_t smem_bytes(int nh) {
-  return 1024 + (uint32_t)(kBlocks * nh * 128 + kStages * kStageBytes + nh * 128) + (uint32_t)sizeof(Misc);
+  return 1024 + (uint32_t)(kBlocks * nh * 128 + kStages * kStageBytes + kPBytes) + (uint32_t)sizeof(Misc);
 }
 static_assert(smem_bytes(kTcHeads) <= 227 * 1024, "one block's shared memory");
 
@@ -126,7 +127,6 @@ struct Walk {
 
 __global__ void __launch_bounds__(kThreads, 1)
     k_attn_tc(const __grid_constant__ AttnArgs a) {
-  pdl_enter();
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int NH = a.group, H = a.H;
@@ -135,7 +135,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* q_sm = smem;
   uint8_t* kv_sm = q_sm + kBlocks * NH * 128;
   uint8_t* p_sm = kv_sm + kStages * kStageBytes;
-  Misc& ms = *reinterpret_cast<Misc*>(p_sm + NH * 128);
+  Misc& ms = *reinterpret_cast<Misc*>(p_sm + kPBytes);
   const uint32_t q_at = smem_u32(q_sm), kv_at = smem_u32(kv_sm), p_at = smem_u32(p_sm);
   Bars& B = ms.bars;
   auto bar = [](uint64_t& b) { return smem_u32(&b); };
@@ -144,25 +144,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int g = blockIdx.x % a.ngroups, u = blockIdx.x / a.ngroups;
   const int h0 = g * NH;
 
-  // the block's items and units (all threads)
-  Walk w;
-  {
-    int* tmp = reinterpret_cast<int*>(ms.info);
-    const int total = attn_units_before(a, a.Q * a.rows, tmp), ranges = min(a.ranges, total);
-    w.whole = a.whole;
-    w.later = 0;
-    w.at = w.stop = w.first = 0;
-    if (u < ranges) {
-      w.at = range_begin(total, ranges, u);
-      w.stop = range_begin(total, ranges, u + 1);
-      w.later = attn_item_of(a, w.at, tmp, &w.first);
-    }
-    w.item = w.whole ? u * w.whole : w.later;
-    __syncthreads();
-  }
-  if (!w.whole && w.at >= w.stop) return;
-  const int my_begin = w.at;
-
+  // what does not depend on the kernel before runs while that ends
   if (threadIdx.x == 0) {
     ms.abort_flag = 0;
     for (int s = 0; s < kStages; ++s)
@@ -191,8 +173,32 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   fence_after();
   const uint32_t tmem = ms.tmem;
+  pdl_enter();
 
-  if (warp == kLookWarp) {
+  // the block's items and units (all threads)
+  Walk w;
+  {
+    int* tmp = reinterpret_cast<int*>(ms.info);
+    const int total = attn_units_before(a, a.Q * a.rows, tmp), ranges = min(a.ranges, total);
+    w.whole = a.whole;
+    w.later = 0;
+    w.at = w.stop = w.first = 0;
+    if (u < ranges) {
+      w.at = range_begin(total, ranges, u);
+      w.stop = range_begin(total, ranges, u + 1);
+      w.later = attn_item_of(a, w.at, tmp, &w.first);
+    }
+    w.item = w.whole ? u * w.whole : w.later;
+    __syncthreads();
+  }
+  const int my_begin = w.at;
+  const bool any = w.whole || w.at < w.stop;
+
+
+
+  if (!any) {
+    // more blocks than units
+  } else if (warp == kLookWarp) {
     // ======================= look-up =======================
     // Lane l takes tokens 2 l and 2 l + 1, two units at a time.
     const LatentCache& C = a.cache;
@@ -467,8 +473,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool alive = true;
       do {
         // ---- scores of the tile ----
-        bool ok = wait_warp2(bar(B.info[tile % kInfo]), (uint32_t)(tile / kInfo) & 1u, bar(B.sfull[tile & 1]),
-                             (uint32_t)(tile >> 1) & 1u, ctl);
+        // (S of the tile, and the weights' place: the second product of the tile before has read it, and O is whole)
+        bool ok = wait_warp3(bar(B.info[tile % kInfo]), (uint32_t)(tile / kInfo) & 1u, bar(B.sfull[tile & 1]),
+                             (uint32_t)(tile >> 1) & 1u, bar(B.pempty), (uint32_t)tile & 1u ^ 1u, ctl);
         uint32_t s[16], p[8];
         flags = 0;
         if (ok) {
@@ -518,8 +525,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             grow = x0 > (m0 == -INFINITY ? -INFINITY : kLazy) || x1 > (m1 == -INFINITY ? -INFINITY : kLazy);
           }
           if (pass || !bar_or(1, kSoft, grow || !ok)) break;
-          // (the second product of the tile before has read the weights and O is whole)
-          if (ok && tile > 0) ok = wait_warp(bar(B.pempty), (uint32_t)(tile - 1) & 1u, ctl);
           float t0 = -INFINITY, t1 = -INFINITY;
           if (ok && mine) {
 #pragma unroll
@@ -578,8 +583,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!alive) break;
         l0 += d0;
         l1 += d1;
-        ok = tile == 0 || wait_warp(bar(B.pempty), (uint32_t)(tile - 1) & 1u, ctl);
-        if (ok && mine) {
+        if (mine) {
 #pragma unroll
           for (int n = 0; n < 4; ++n) {
             const uint32_t at = prow + (uint32_t)(((4 * half + n) ^ sw) << 4);
@@ -588,10 +592,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           fence_async_smem();
         }
-        // a wait that ran out here is met again at the next tile's barrier or the item's end
         fence_before();
         __syncwarp();
-        if (ok && lane == 0) mbar_arrive(bar(B.pfull));
+        if (lane == 0) mbar_arrive(bar(B.pfull));
         ++tile;
       } while (!(flags & 2));
       if (!alive) break;
@@ -627,38 +630,43 @@ __global__ void __launch_bounds__(kThreads, 1)
       bar_sync(1, kSoft);
       fence_after();
       const int nh = min(NH, H - h0);
-      // 16 heads x 128 columns at a time, the next ones' load in flight; the two halves take 256 columns each
-      const int steps = 2 * (NH / 16);
-      const uint32_t o_at = tmem + lanes + (uint32_t)(2 * half * NH);
-      uint32_t o[2][16];
-      tmem_ld16(o_at, o[0]);
-      auto put = [&](int i, const uint32_t (&o)[16]) {
-        const int mb = i * 16 / NH, c = i * 16 - mb * NH, d = (2 * half + mb) * 128 + quarter * 32 + lane;
-        if (whole) {
-          __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(a.out) +
-                               ((int64_t)w.item * H + h0 + c + (lane & 1)) * kDC + (d & ~1);
-#pragma unroll
-          for (int k = 0; k < 16; k += 2) {
-            // neighbouring lanes trade halves: each gets two columns of one head
-            const float x = __uint_as_float(o[k]) * ms.fac[c + k], y = __uint_as_float(o[k + 1]) * ms.fac[c + k + 1];
-            const float z = __shfl_xor_sync(0xffffffffu, (lane & 1) ? x : y, 1);
-            if (c + k + (lane & 1) < nh)
-              *reinterpret_cast<uint32_t*>(out + (int64_t)k * kDC) = (lane & 1) ? pack_bf16(z, y) : pack_bf16(x, z);
-          }
-        } else {
-          float* out = a.part + (part * NH + c) * kDC + d;
-#pragma unroll
-          for (int k = 0; k < 16; ++k) out[k * kDC] = __uint_as_float(o[k]);
-        }
-      };
+      // 16 heads x 128 columns at a time; the two halves take 256 columns each
+      __nv_bfloat16* turn = reinterpret_cast<__nv_bfloat16*>(p_sm) + half * 16 * 128;  // [16 heads][128 columns]
+      const int t128 = threadIdx.x & 127;
 #pragma unroll 1
-      for (int i = 0; i < steps; i += 2) {  // steps is even
+      for (int i = 0; i < 2 * NH; i += 16) {
+        uint32_t o[16];
+        tmem_ld16(tmem + lanes + (uint32_t)(2 * half * NH + i), o);
+        const int mb = i >= NH, c = i - mb * NH, d = (2 * half + mb) * 128;
         tmem_wait_ld();
-        tmem_ld16(o_at + (uint32_t)(i + 1) * 16, o[1]);
-        put(i, o[0]);
-        tmem_wait_ld();
-        if (i + 2 < steps) tmem_ld16(o_at + (uint32_t)(i + 2) * 16, o[0]);
-        put(i + 1, o[1]);
+        if (whole) {
+          // 16 bytes a thread, by way of the weights' place
+          float4 f[4];  // (all read before the first store, which might alias them)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) f[k] = *reinterpret_cast<const float4*>(ms.fac + c + 4 * k);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            __nv_bfloat16* at = turn + 4 * k * 128 + quarter * 32 + lane;
+            at[0] = __float2bfloat16_rn(__uint_as_float(o[4 * k]) * f[k].x);
+            at[128] = __float2bfloat16_rn(__uint_as_float(o[4 * k + 1]) * f[k].y);
+            at[256] = __float2bfloat16_rn(__uint_as_float(o[4 * k + 2]) * f[k].z);
+            at[384] = __float2bfloat16_rn(__uint_as_float(o[4 * k + 3]) * f[k].w);
+          }
+          bar_sync(2 + half, 128);
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const int k = 8 * j + (t128 >> 4), col = (t128 & 15) * 8;
+            if (c + k < nh)
+              *reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(a.out) +
+                                        ((int64_t)w.item * H + h0 + c + k) * kDC + d + col) =
+                  *reinterpret_cast<const uint4*>(turn + k * 128 + col);
+          }
+          bar_sync(2 + half, 128);
+        } else {
+          float* sh = a.part + (part * NH + c) * kDC + d + quarter * 32 + lane;
+#pragma unroll
+          for (int k = 0; k < 16; ++k) sh[k * kDC] = __uint_as_float(o[k]);
+        }
       }
       fence_before();
       __syncwarp();
@@ -679,7 +687,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 bool attn_tc_supported(const AttnArgs& a, int bf16) {
   // cache rows are 32-bit numbers
   return bf16 && a.cache.dc == kDC && a.cache.dr == kDR && ((uintptr_t)a.cache.data & 15) == 0 &&
-         ((int64_t)a.cache.num_pages << a.cache.log2b) < (int64_t(1) << 31) && ((uintptr_t)a.out & 3) == 0;
+         ((int64_t)a.cache.num_pages << a.cache.log2b) < (int64_t(1) << 31) && ((uintptr_t)a.out & 15) == 0;
 }
 
 cudaError_t launch_attn_tc(const AttnArgs& a, cudaStream_t s) {

@@ -96,6 +96,11 @@ __device__ __forceinline__ bool wait_warp2(uint32_t bar0, uint32_t parity0, uint
   const bool odd = threadIdx.x & 1;
   return __all_sync(0xffffffffu, wait(odd ? bar1 : bar0, odd ? parity1 : parity0, c));
 }
+__device__ __forceinline__ bool wait_warp3(uint32_t bar0, uint32_t parity0, uint32_t bar1, uint32_t parity1,
+                                           uint32_t bar2, uint32_t parity2, Ctl c) {
+  const int i = threadIdx.x & 3;
+  return __all_sync(0xffffffffu, wait(i == 0 ? bar0 : i == 1 ? bar1 : bar2, i == 0 ? parity0 : i == 1 ? parity1 : parity2, c));
+}
 // One lane of a converged warp.  tcgen05.mma and its descriptors live on the
 // uniform datapath: issued by the elected lane of a warp whose control flow
 // is uniform, an instruction costs a few cycles; issued under `lane == 0` it
