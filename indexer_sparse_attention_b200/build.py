@@ -12,7 +12,7 @@ BUILD_DIR = os.path.join(ROOT, "_build")
 SO = os.path.join(HERE, "libspin.so")
 SOURCES = ["spin_api.cu", "k_select.cu", "k_score_simt.cu", "k_score_tc.cu", "k_topk.cu", "k_ema.cu",
            "spin_noalloc.cu", "k_quality.cu", "latent_api.cu", "k_rope.cu", "k_latent_simt.cu",
-           "k_latent_tc.cu"]
+           "k_latent_tc.cu", "k_prefill_tc.cu"]
 HEADERS = ["spin_internal.cuh", "block_scan.cuh", "latent_internal.cuh", "umma.cuh"]
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-lineinfo", "-std=c++17",

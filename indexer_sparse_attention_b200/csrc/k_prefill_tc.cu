@@ -1,0 +1,675 @@
+// k_prefill_tc.cu -- expanded latent attention on the 5th-generation tensor
+// cores: bf16, latent width 512, key width 128 + 64 (rotary), value width 128.
+//
+// k_expand_tc   [k | v] = W_h c for every slot and head, into the workspace: a
+//               matrix product M = slots, N = 256, K = 512.  A block keeps the
+//               latents of 128 slots (128 KB) and streams the heads' weights, so
+//               L2 -> SM carries 256 KB a 4096-cycle tile instead of 384.
+// k_prefill_tc  causal attention of 256 rows of one head: two 128-row tiles take
+//               turns on the tensor cores, one's softmax under the other's
+//               products:
+//   S_t [128 x 128 keys] = Q_t . K^T   M 128, N 128, K 192 (shared memory both)
+//   O_t [128 x 128]     += P_t . V     M 128, N 64 x 2, K 128 (P from TMEM)
+//               P (bf16) overwrites its S in TMEM.  A thread owns a row, so
+//               maximum, sum and rescaling need no exchange; the softmax
+//               reference moves only where a row's maximum has grown by more
+//               than 8 (log2 units), and then its warp rescales O.  K and V come
+//               as 16 KB blocks of 64 columns through one ring of eight, in the
+//               order of use.
+#include "latent_internal.cuh"
+#include "umma.cuh"
+
+namespace spin {
+namespace {
+
+using namespace umma;
+
+constexpr int kDC = 512, kDR = 64, kDN = 128, kDV = 128, kN = kDN + kDV;
+constexpr int kRowTile = 128;
+constexpr int kBlk = kRowTile * 128;  // 128 rows of 64 columns
+constexpr float kLazy = 8.0f;
+
+// ---------------------------------------------------------------------------
+// expansion
+// ---------------------------------------------------------------------------
+constexpr int kExpThreads = 192;     // warps 0..3 epilogue, 4 copies, 5 MMA issue
+constexpr int kABlocks = kDC / 64;   // 8
+constexpr int kBBytes = kN * 128;    // 256 weights' rows of 64 columns
+constexpr int kBStages = 2;
+constexpr int kOutBufs = 2;          // 16 KB blocks on their way out
+
+struct ExpMisc {
+  uint64_t afull[kABlocks], afree;   // latents of a slot tile
+  uint64_t bfull[kBStages], bfree[kBStages];
+  uint64_t dfull[2], dfree[2];       // accumulators
+  uint64_t done;
+  int tmp[35];
+  uint32_t tmem;
+  int abort_flag;
+};
+constexpr uint32_t kExpSmem = 1024 + kABlocks * kBlk + kBStages * kBBytes + kOutBufs * kBlk + sizeof(ExpMisc);
+static_assert(kExpSmem <= 227 * 1024, "one block's shared memory");
+
+// The walk over units (slot tile, head), heads within a tile.
+struct ExpWalk {
+  int q, tile, h;   // request, its slot tile, head
+  int tiles, end;   // the request's
+  int64_t off;      // its first workspace row
+  __device__ __forceinline__ void open(const PrefillArgs& a) {
+    const Chunk c = prefill_chunk(a, q, false);
+    end = c.end;
+    tiles = (c.end + kSlotTile - 1) / kSlotTile;
+  }
+  __device__ __forceinline__ void step(const PrefillArgs& a) {
+    if (++h < a.H) return;
+    h = 0;
+    ++tile;
+    while (tile >= tiles) {  // (a caller that steps past the last unit does not look further)
+      off += (int64_t)tiles * kSlotTile;
+      tile = 0;
+      if (++q >= a.Q) return;
+      open(a);
+    }
+  }
+};
+
+__global__ void __launch_bounds__(kExpThreads, 1)
+    k_expand_tc(const __grid_constant__ PrefillArgs a, const __grid_constant__ CUtensorMap map_c,
+                const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_kv) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* a_sm = smem;
+  uint8_t* b_sm = a_sm + kABlocks * kBlk;
+  uint8_t* o_sm = b_sm + kBStages * kBBytes;
+  ExpMisc& ms = *reinterpret_cast<ExpMisc*>(o_sm + kOutBufs * kBlk);
+  const uint32_t a_at = smem_u32(a_sm), b_at = smem_u32(b_sm), o_at = smem_u32(o_sm);
+  auto bar = [](uint64_t& b) { return smem_u32(&b); };
+  const Ctl ctl{&ms.abort_flag, a.err};
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    ms.abort_flag = 0;
+    for (int i = 0; i < kABlocks; ++i) mbar_init(bar(ms.afull[i]), 1);
+    mbar_init(bar(ms.afree), 1);
+    for (int i = 0; i < kBStages; ++i) {
+      mbar_init(bar(ms.bfull[i]), 1);
+      mbar_init(bar(ms.bfree[i]), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(ms.dfull[i]), 1);
+      mbar_init(bar(ms.dfree[i]), 4);
+    }
+    mbar_init(bar(ms.done), 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 5) tmem_alloc(smem_u32(&ms.tmem), 512);
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = ms.tmem;
+  pdl_enter();
+
+  // This block's units.  Requests in order; one that does not fit the
+  // workspace ends the list (those behind it do not fit either).
+  ExpWalk w{};
+  int n_units = 0;
+  {
+    int total = 0, tiles_before = 0;  // units; all fit 31 bits (the host's check)
+    int carry = 0;
+    for (int base = 0; base < a.Q; base += kExpThreads) {
+      const int q = base + (int)threadIdx.x;
+      const int t = q < a.Q ? (prefill_chunk(a, q, blockIdx.x == 0).end + kSlotTile - 1) / kSlotTile : 0;
+      int sum;
+      const int ex = carry + block_exclusive_scan(t, ms.tmp, &sum);
+      const bool fits = (int64_t)(ex + t) * kSlotTile <= a.cap;
+      if (q < a.Q && t && !fits && blockIdx.x == 0) raise_error(a.err, ERR_CAPACITY, q, (uint32_t)t * kSlotTile);
+      int kept;
+      block_exclusive_scan(fits ? t : 0, ms.tmp, &kept);
+      total += kept;
+      carry += sum;
+    }
+    total *= a.H;
+    const int u0 = range_begin(total, gridDim.x, blockIdx.x), u1 = range_begin(total, gridDim.x, blockIdx.x + 1);
+    n_units = u1 - u0;
+    // the request that holds unit u0
+    const int want = u0 / a.H;
+    carry = 0;
+    for (int base = 0; base < a.Q && n_units; base += kExpThreads) {
+      const int q = base + (int)threadIdx.x;
+      const int t = q < a.Q ? (prefill_chunk(a, q, false).end + kSlotTile - 1) / kSlotTile : 0;
+      int sum;
+      const int ex = carry + block_exclusive_scan(t, ms.tmp, &sum);
+      if (ex <= want && want < ex + t) {
+        ms.tmp[33] = q;
+        ms.tmp[34] = ex;
+      }
+      carry += sum;
+      if (carry > want) break;
+    }
+    __syncthreads();
+    if (n_units) {
+      w.q = ms.tmp[33];
+      tiles_before = ms.tmp[34];
+      w.off = (int64_t)tiles_before * kSlotTile;
+      w.tile = want - tiles_before;
+      w.h = u0 - want * a.H;
+      w.open(a);
+    }
+  }
+
+  if (!n_units) {
+    // more blocks than units
+  } else if (warp == 4) {
+    // ======================= copies =======================
+    const LatentCache& C = a.cache;
+    const int box = min(C.b, kSlotTile), boxes = kSlotTile / box;  // rows of a copy, copies a block
+    const int none = C.num_pages << C.log2b;                       // a row outside the cache: zeros
+    int st = 0, seen = -1, q_seen = -1, nload = 0;
+    uint32_t ph = 0;
+    bool ok = true;
+    uint32_t a_armed = 0, b_armed[kBStages] = {2, 2};
+    for (int i = 0; i < n_units && ok; ++i) {
+      if (w.tile != seen || w.q != q_seen) {
+        seen = w.tile;
+        q_seen = w.q;
+        int row = none;
+        const int slot = w.tile * kSlotTile + lane * box;
+        if (lane < boxes && slot < w.end) {
+          const int page = C.bt[(int64_t)w.q * C.bt_stride + (slot >> C.log2b)];
+          if (page >= 0 && page < C.num_pages)
+            row = (page << C.log2b) + (slot & (C.b - 1));
+          else
+            raise_error(a.err, ERR_PAGE, w.q, (uint32_t)page);
+        }
+        ok = wait_warp(bar(ms.afree), (uint32_t)nload & 1u ^ 1u, ctl);
+        if (!ok) break;
+        if (lane == 0)
+          for (int k = 0; k < kABlocks; ++k) mbar_expect_tx(bar(ms.afull[k]), kBlk);
+        ++nload;
+        a_armed = 1;
+        __syncwarp();
+        if (lane < boxes)
+          for (int k = 0; k < kABlocks; ++k)
+            tma_load_2d(a_at + k * kBlk + lane * box * 128, &map_c, bar(ms.afull[k]), k * 64, row);
+      }
+      for (int k = 0; k < kABlocks; ++k) {
+        ok = wait_warp(bar(ms.bfree[st]), ph ^ 1u, ctl);
+        if (!ok) break;
+        if (lane == 0) {
+          mbar_expect_tx(bar(ms.bfull[st]), kBBytes);
+          tma_load_2d(b_at + st * kBBytes, &map_w, bar(ms.bfull[st]), k * 64, w.h * kN);
+        }
+        b_armed[st] = ph;
+        if (++st == kBStages) {
+          st = 0;
+          ph ^= 1u;
+        }
+      }
+      w.step(a);
+    }
+    if (lane == 0 && ms.abort_flag) {
+      if (a_armed)
+        for (int k = 0; k < kABlocks; ++k) drain(bar(ms.afull[k]), (uint32_t)(nload - 1) & 1u);
+      for (int s = 0; s < kBStages; ++s)
+        if (b_armed[s] < 2) drain(bar(ms.bfull[s]), b_armed[s]);
+    }
+  } else if (warp == 5) {
+    // ======================= MMA issue =======================
+    const uint32_t id = idesc_bf16(128, kN, 0, 0);
+    int st = 0, nload = -1, seen = -1, q_seen = -1;
+    uint32_t ph = 0;
+    bool ok = true;
+    for (int i = 0; i < n_units && ok; ++i) {
+      const bool fresh = w.tile != seen || w.q != q_seen;
+      if (fresh) {
+        seen = w.tile;
+        q_seen = w.q;
+        ++nload;
+      }
+      const uint32_t d = tmem + (uint32_t)(i & 1) * kN;
+      ok = wait_warp(bar(ms.dfree[i & 1]), (uint32_t)(i >> 1) & 1u ^ 1u, ctl);
+      for (int k = 0; k < kABlocks && ok; ++k) {
+        if (fresh) ok = wait_warp(bar(ms.afull[k]), (uint32_t)nload & 1u, ctl);
+        ok = ok && wait_warp(bar(ms.bfull[st]), ph, ctl);
+        if (!ok) break;
+        fence_after();
+        const uint64_t ad = sw128_desc(a_at + k * kBlk, 16, 1024), bd = sw128_desc(b_at + st * kBBytes, 16, 1024);
+        if (elect()) {
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) mma_f16(d, ad + 2 * kk, bd + 2 * kk, id, k > 0 || kk > 0 ? 1u : 0u);
+          commit(bar(ms.bfree[st]));
+        }
+        __syncwarp();
+        if (++st == kBStages) {
+          st = 0;
+          ph ^= 1u;
+        }
+      }
+      if (!ok) break;
+      w.step(a);
+      const bool leave = i + 1 < n_units && (w.tile != seen || w.q != q_seen);
+      if (elect()) {
+        commit(bar(ms.dfull[i & 1]));
+        if (leave) commit(bar(ms.afree));
+      }
+      __syncwarp();
+    }
+    if (elect()) commit(bar(ms.done));
+    __syncwarp();
+    drain(bar(ms.done), 0);
+  } else {
+    // ======================= epilogue =======================
+    const int row = warp * 32 + lane;
+    const uint32_t lanes = (uint32_t)(warp * 32) << 16;
+    const LatentCache& C = a.cache;
+    int buf = 0;
+    for (int i = 0; i < n_units; ++i) {
+      const int slot = w.tile * kSlotTile + row;
+      const bool live = slot < w.end;  // rows past the request's slots become zeros: a weight of 0 must meet no NaN
+      if (w.h == 0) {
+        uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(a.kr) + (w.off + slot) * kDR);
+        const uint4* src = nullptr;
+        if (live) {
+          const int page = C.bt[(int64_t)w.q * C.bt_stride + (slot >> C.log2b)];
+          if (page >= 0 && page < C.num_pages)
+            src = reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(C.data) +
+                                                 (((int64_t)page << C.log2b) + (slot & (C.b - 1))) * (kDC + kDR) + kDC);
+        }
+#pragma unroll
+        for (int c = 0; c < kDR / 8; ++c) dst[c] = src ? src[c] : make_uint4(0, 0, 0, 0);
+      }
+      const bool ok = wait_warp(bar(ms.dfull[i & 1]), (uint32_t)(i >> 1) & 1u, ctl);
+      if (bar_or(1, 128, !ok)) break;  // (the warps leave together: they meet at barriers below)
+      fence_after();
+#pragma unroll 1
+      for (int c = 0; c < kN / 64; ++c) {
+        uint32_t v[2][32];
+        tmem_ld32(tmem + lanes + (uint32_t)((i & 1) * kN + c * 64), v[0]);
+        tmem_ld32(tmem + lanes + (uint32_t)((i & 1) * kN + c * 64 + 32), v[1]);
+        tmem_wait_ld();
+        // the block's buffer: its store two blocks ago has read it
+        if (threadIdx.x == 0) asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kOutBufs - 1) : "memory");
+        bar_sync(1, 128);
+        const uint32_t dst = o_at + buf * kBlk + row * 128;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          uint32_t p[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int x = 8 * j + 2 * e;
+            p[e] = live ? pack_bf16(__uint_as_float(v[x >> 5][x & 31]), __uint_as_float(v[x >> 5][(x & 31) + 1])) : 0u;
+          }
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + ((j ^ (row & 7)) << 4)), "r"(p[0]),
+                       "r"(p[1]), "r"(p[2]), "r"(p[3])
+                       : "memory");
+        }
+        if (c == kN / 64 - 1) {  // the accumulator is in registers: hand it back
+          fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(ms.dfree[i & 1]));
+        }
+        fence_async_smem();
+        bar_sync(1, 128);
+        if (threadIdx.x == 0) {
+          asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
+                           (uint64_t)&map_kv),
+                       "r"(o_at + buf * kBlk), "r"(w.h * kN + c * 64), "r"((int)(w.off + w.tile * kSlotTile))
+                       : "memory");
+          asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+        }
+        buf ^= 1;
+      }
+      w.step(a);
+    }
+    if (threadIdx.x == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+  }
+
+  fence_before();
+  __syncthreads();
+  fence_after();
+  if (warp == 5) tmem_dealloc(tmem, 512);
+}
+
+// ---------------------------------------------------------------------------
+// attention
+// ---------------------------------------------------------------------------
+constexpr int kAttThreads = 320;  // warps 0..3 and 4..7 the two row tiles' softmax, 8 copies, 9 MMA issue
+constexpr int kRing = 8;
+constexpr int kKBlocks = 3, kVBlocks = 2, kKV = kKBlocks + kVBlocks;
+
+struct AttMisc {
+  uint64_t full[kRing], empty[kRing];
+  uint64_t qfull[2], sfull[2], pfull[2][2], ofull[2];
+  uint64_t done;
+  int64_t tmp[33];
+  uint32_t tmem;
+  int abort_flag;
+};
+constexpr uint32_t kAttSmem = 1024 + 2 * kKBlocks * kBlk + kRing * kBlk + sizeof(AttMisc);
+static_assert(kAttSmem <= 227 * 1024, "one block's shared memory");
+
+__global__ void __launch_bounds__(kAttThreads, 1)
+    k_prefill_tc(const __grid_constant__ PrefillArgs a, const __grid_constant__ CUtensorMap map_kv,
+                 const __grid_constant__ CUtensorMap map_kr) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* q_sm = smem;
+  uint8_t* r_sm = q_sm + 2 * kKBlocks * kBlk;
+  AttMisc& ms = *reinterpret_cast<AttMisc*>(r_sm + kRing * kBlk);
+  const uint32_t q_at = smem_u32(q_sm), r_at = smem_u32(r_sm);
+  auto bar = [](uint64_t& b) { return smem_u32(&b); };
+  const Ctl ctl{&ms.abort_flag, a.err};
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int h = blockIdx.y, q = blockIdx.z;
+  const int r0 = (gridDim.x - 1 - blockIdx.x) * 2 * kRowTile;  // the longest rows first
+
+  pdl_enter();
+  const Chunk ch = prefill_chunk(a, q, false);
+  if (r0 >= ch.count) return;
+  const int64_t off = prefill_rows_before(a, q, ms.tmp);
+  if (off + ch.end > a.cap) return;
+  {
+    const LatentCache& C = a.cache;
+    int bad = 0;
+    for (int i = threadIdx.x; i <= (ch.end - 1) >> C.log2b; i += kAttThreads) {
+      const int page = C.bt[(int64_t)q * C.bt_stride + i];
+      bad |= page < 0 || page >= C.num_pages;
+    }
+    if (__syncthreads_or(bad)) return;
+  }
+  // rows and key tiles of the two row tiles
+  const int rows0 = min(ch.count - r0, kRowTile), rows1 = max(0, min(ch.count - r0 - kRowTile, kRowTile));
+  const int pos0 = ch.ctx - 1 + r0;  // of the first row
+  const int n0 = (pos0 + rows0 - 1) / kRowTile + 1;
+  const int n1 = rows1 ? (pos0 + kRowTile + rows1 - 1) / kRowTile + 1 : 0;
+  const int n = max(n0, n1);
+
+  if (threadIdx.x == 0) {
+    ms.abort_flag = 0;
+    for (int i = 0; i < kRing; ++i) {
+      mbar_init(bar(ms.full[i]), 1);
+      mbar_init(bar(ms.empty[i]), 1);
+    }
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(bar(ms.qfull[t]), 128);
+      mbar_init(bar(ms.sfull[t]), 1);
+      mbar_init(bar(ms.pfull[t][0]), 4);
+      mbar_init(bar(ms.pfull[t][1]), 4);
+      mbar_init(bar(ms.ofull[t]), 1);
+    }
+    mbar_init(bar(ms.done), 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 9) tmem_alloc(smem_u32(&ms.tmem), 512);
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = ms.tmem;
+  constexpr uint32_t kOCol = 256;
+
+  if (warp == 8) {
+    // ======================= copies =======================
+    uint32_t armed[kRing];
+    for (int i = 0; i < kRing; ++i) armed[i] = 2;
+    bool ok = true;
+    int s = 0;
+    uint32_t ph = 0;
+    for (int i = 0; i < n && ok; ++i) {
+      const int row = (int)(off + (int64_t)i * kRowTile);
+#pragma unroll 1
+      for (int b = 0; b < kKV; ++b) {
+        ok = wait_warp(bar(ms.empty[s]), ph ^ 1u, ctl);
+        if (!ok) break;
+        if (lane == 0) {
+          mbar_expect_tx(bar(ms.full[s]), kBlk);
+          if (b == 2)
+            tma_load_2d(r_at + s * kBlk, &map_kr, bar(ms.full[s]), 0, row);
+          else
+            tma_load_2d(r_at + s * kBlk, &map_kv, bar(ms.full[s]), h * kN + (b < 2 ? b : b - 1) * 64, row);
+        }
+        armed[s] = ph;
+        if (++s == kRing) {
+          s = 0;
+          ph ^= 1u;
+        }
+      }
+    }
+    if (lane == 0 && ms.abort_flag)
+      for (int i = 0; i < kRing; ++i)
+        if (armed[i] < 2) drain(bar(ms.full[i]), armed[i]);
+  } else if (warp == 9) {
+    // ======================= MMA issue =======================
+    const uint32_t id_s = idesc_bf16(128, 128, 0, 0), id_o = idesc_bf16(128, 64, 0, 1);
+    bool ok = true;
+    // ring blocks of K(i): 5 i .. + 2, of V(i): 5 i + 3, 5 i + 4
+    auto first = [&](int t, int i) {  // S_t(i)
+      const bool last = t == (i < n1 ? 1 : 0);
+#pragma unroll
+      for (int b = 0; b < kKBlocks; ++b) {
+        const int x = kKV * i + b, s = x % kRing;
+        ok = ok && wait_warp(bar(ms.full[s]), (uint32_t)(x / kRing) & 1u, ctl);
+        if (!ok) return;
+        fence_after();
+        const uint64_t ad = sw128_desc(q_at + (t * kKBlocks + b) * kBlk, 16, 1024);
+        const uint64_t bd = sw128_desc(r_at + s * kBlk, 16, 1024);
+        if (elect()) {
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            mma_f16(tmem + t * 128, ad + 2 * kk, bd + 2 * kk, id_s, b > 0 || kk > 0 ? 1u : 0u);
+          if (last) commit(bar(ms.empty[s]));
+          if (b == kKBlocks - 1) commit(bar(ms.sfull[t]));
+        }
+        __syncwarp();
+      }
+    };
+    auto second = [&](int t, int i) {  // O_t += P_t(i) V(i)
+      const bool last = t == (i < n1 ? 1 : 0);
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        ok = ok && wait_warp(bar(ms.pfull[t][half]), (uint32_t)i & 1u, ctl);
+        if (!ok) return;
+#pragma unroll
+        for (int b = 0; b < kVBlocks; ++b) {
+          const int x = kKV * i + kKBlocks + b, s = x % kRing;
+          if (half == 0) ok = ok && wait_warp(bar(ms.full[s]), (uint32_t)(x / kRing) & 1u, ctl);
+          if (!ok) return;
+          fence_after();
+          const uint64_t bd = sw128_desc(r_at + s * kBlk, kBlk, 1024);
+          if (elect()) {
+#pragma unroll
+            for (int kk = 4 * half; kk < 4 * half + 4; ++kk)
+              mma_f16_ts(tmem + kOCol + t * 128 + b * 64, tmem + t * 128 + kk * 8, bd + kk * (2048 >> 4), id_o,
+                         i > 0 || kk > 0 ? 1u : 0u);
+            if (last && half == 1) commit(bar(ms.empty[s]));
+          }
+          __syncwarp();
+        }
+      }
+      if (i + 1 == (t ? n1 : n0)) {
+        if (elect()) commit(bar(ms.ofull[t]));
+        __syncwarp();
+      }
+    };
+#pragma unroll 1
+    for (int t = 0; t < 2; ++t)
+      if (t == 0 || n1) {
+        ok = ok && wait_warp(bar(ms.qfull[t]), 0, ctl);
+        if (ok) first(t, 0);
+      }
+#pragma unroll 1
+    for (int i = 0; i < n && ok; ++i)
+#pragma unroll 1
+      for (int t = 0; t < 2; ++t) {
+        const int nt = t ? n1 : n0;
+        if (ok && i < nt) second(t, i);
+        if (ok && i + 1 < nt) first(t, i + 1);
+      }
+    if (elect()) commit(bar(ms.done));
+    __syncwarp();
+    drain(bar(ms.done), 0);
+  } else {
+    // ======================= softmax and output =======================
+    const int t = warp >> 2, tid = threadIdx.x & 127;
+    const int nt = t ? n1 : n0, rows = t ? rows1 : rows0;
+    const int64_t token0 = (int64_t)q * a.rows + r0 + t * kRowTile;
+    if (nt) {
+      // the tile's queries: 8 lanes a 128-byte line, rows behind the last as zeros
+      const int piece = tid & 7;
+#pragma unroll 1
+      for (int row = tid >> 3; row < kRowTile; row += 16) {
+        const bool live = row < rows;
+        const char* src = reinterpret_cast<const char*>(a.q) +
+                          ((live ? (token0 + row) * a.q_tok : 0) + h * a.q_head) * 2 + piece * 16;
+        const uint32_t dst = q_at + t * kKBlocks * kBlk + row * 128 + ((piece ^ (row & 7)) << 4);
+        if (a.q_vec) {
+#pragma unroll
+          for (int b = 0; b < kKBlocks; ++b)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + b * kBlk), "l"(src + b * 128),
+                         "r"(live ? 16u : 0u)
+                         : "memory");
+        } else {
+#pragma unroll 1
+          for (int b = 0; b < kKBlocks; ++b) {
+            const uint16_t* e = reinterpret_cast<const uint16_t*>(src + b * 128);
+            uint32_t v[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) v[k] = live ? (uint32_t)e[2 * k] | (uint32_t)e[2 * k + 1] << 16 : 0u;
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + b * kBlk), "r"(v[0]), "r"(v[1]),
+                         "r"(v[2]), "r"(v[3])
+                         : "memory");
+          }
+        }
+      }
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      fence_async_smem();
+      mbar_arrive(bar(ms.qfull[t]));
+    }
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t s_at = tmem + lanes + t * 128, o_at = tmem + lanes + kOCol + t * 128;
+    const int pos = pos0 + t * kRowTile + tid;        // this thread's row
+    const int whole = (pos0 + t * kRowTile + 1) / kRowTile;  // key tiles that every row of the tile sees whole
+    const float scale = a.scale_log2;
+    float m = -INFINITY, l = 0.f;
+    bool ok = true;
+    for (int i = 0; i < nt; ++i) {
+      // (S of this tile follows the second product of the tile before: O is whole)
+      ok = wait_warp(bar(ms.sfull[t]), (uint32_t)i & 1u, ctl);
+      if (!ok) break;
+      fence_after();
+      uint32_t s[4][32];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) tmem_ld32(s_at + c * 32, s[c]);
+      tmem_wait_ld();
+      if (i >= whole) {
+        const int left = pos - i * kRowTile;  // columns 0 .. left are seen
+#pragma unroll
+        for (int c = 0; c < 128; ++c)
+          if (c > left) s[c >> 5][c & 31] = 0xff800000u;
+      }
+      float mt[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+      for (int c = 0; c < 32; ++c)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) mt[k] = fmaxf(mt[k], __uint_as_float(s[k][c]));
+      const float top = fmaxf(fmaxf(mt[0], mt[1]), fmaxf(mt[2], mt[3])) * scale;
+      if (__any_sync(0xffffffffu, top > m + kLazy)) {  // (true at the first tile: m is -inf)
+        const float mn = fmaxf(m, top);
+        const float f = mn == -INFINITY ? 1.f : ex2(m - mn);
+        m = mn;
+        l *= f;
+        if (i > 0) {
+#pragma unroll 1
+          for (int c = 0; c < 8; ++c) {
+            uint32_t o[16];
+            tmem_ld16(o_at + c * 16, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+            tmem_st16(o_at + c * 16, o);
+          }
+        }
+      }
+      const float ref = m == -INFINITY ? 0.f : m;
+      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        uint32_t p[32];
+#pragma unroll
+        for (int c = 0; c < 32; ++c) {
+          const int x = 64 * half + 2 * c;
+          const float p0 = ex2(fmaf(__uint_as_float(s[x >> 5][x & 31]), scale, -ref));
+          const float p1 = ex2(fmaf(__uint_as_float(s[x >> 5][(x & 31) + 1]), scale, -ref));
+          sum[c & 3] += p0 + p1;
+          p[c] = pack_bf16(p0, p1);
+        }
+        tmem_st32(s_at + half * 32, p);
+        tmem_wait_st();
+        fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(ms.pfull[t][half]));
+      }
+      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+    }
+    if (ok && nt) ok = wait_warp(bar(ms.ofull[t]), 0, ctl);
+    if (ok && nt) {
+      fence_after();
+      const float norm = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+      __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(a.out) + ((token0 + tid) * a.H + h) * kDV;
+#pragma unroll 1
+      for (int c = 0; c < 4; ++c) {
+        uint32_t o[32];
+        tmem_ld32(o_at + c * 32, o);
+        tmem_wait_ld();
+        if (tid < rows) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            uint32_t v[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              v[e] = pack_bf16(__uint_as_float(o[8 * k + 2 * e]) * norm, __uint_as_float(o[8 * k + 2 * e + 1]) * norm);
+            *reinterpret_cast<uint4*>(out + c * 32 + k * 8) = make_uint4(v[0], v[1], v[2], v[3]);
+          }
+        }
+      }
+    }
+  }
+
+  fence_before();
+  __syncthreads();
+  fence_after();
+  if (warp == 9) tmem_dealloc(tmem, 512);
+}
+
+}  // namespace
+
+bool prefill_tc_supported(const PrefillArgs& a, int bf16) {
+  // rows are the tensor maps' 32-bit coordinates; units fit 31 bits
+  return bf16 && a.cache.dc == kDC && a.cache.dr == kDR && a.dn == kDN && a.dv == kDV &&
+         ((uintptr_t)a.cache.data & 15) == 0 && ((uintptr_t)a.w & 15) == 0 && ((uintptr_t)a.out & 15) == 0 &&
+         ((int64_t)a.cache.num_pages << a.cache.log2b) < (int64_t(1) << 31) - kSlotTile &&
+         a.cap * a.H < (int64_t(1) << 31);
+}
+
+cudaError_t launch_prefill_tc(const PrefillArgs& a, void* encode_fn, int sms, cudaStream_t s) {
+  CUtensorMap mc, mw, mkv, mkr;
+  const uint64_t rows = (uint64_t)a.cache.num_pages << a.cache.log2b;
+  const uint32_t box = (uint32_t)(a.cache.b < kSlotTile ? a.cache.b : kSlotTile);
+  if (!encode_rows(encode_fn, &mc, a.cache.data, rows, kDC + kDR, (kDC + kDR) * 2, box) ||
+      !encode_rows(encode_fn, &mw, a.w, (uint64_t)a.H * kN, kDC, kDC * 2, kN) ||
+      !encode_rows(encode_fn, &mkv, a.kv, (uint64_t)a.cap, (uint64_t)a.H * kN, (uint64_t)a.H * kN * 2, kRowTile) ||
+      !encode_rows(encode_fn, &mkr, a.kr, (uint64_t)a.cap, kDR, kDR * 2, kRowTile))
+    return cudaErrorInvalidValue;
+  cudaError_t e = cudaFuncSetAttribute(k_expand_tc, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kExpSmem);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(k_prefill_tc, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kAttSmem);
+  if (e != cudaSuccess) return e;
+  {
+    PdlLaunch l(dim3((unsigned)sms), dim3(kExpThreads), kExpSmem, s);
+    e = cudaLaunchKernelEx(&l.cfg, k_expand_tc, a, mc, mw, mkv);
+  }
+  if (e != cudaSuccess) return e;
+  PdlLaunch l(dim3((unsigned)((a.rows + 2 * kRowTile - 1) / (2 * kRowTile)), (unsigned)a.H, (unsigned)a.Q),
+              dim3(kAttThreads), kAttSmem, s);
+  return cudaLaunchKernelEx(&l.cfg, k_prefill_tc, a, mkv, mkr);
+}
+
+}  // namespace spin

@@ -361,6 +361,10 @@ spin_status spin_latent_prefill(spin_latent lt, int rows, const void* cache, int
   a.scale_log2 = (float)((double)c.softmax_scale * 1.4426950408889634);
   a.err = lt->err;
   const int bf16 = c.dtype == SPIN_BF16;
+  const int64_t per16 = bf16 ? 8 : 4;
+  a.q_vec = ((uintptr_t)q & 15) == 0 && q_token_stride % per16 == 0 && q_head_stride % per16 == 0;
+  if (lt->encode_fn && prefill_tc_supported(a, bf16))
+    return cuda_status(launch_prefill_tc(a, lt->encode_fn, lt->sms, (cudaStream_t)stream));
   cudaError_t e = launch_expand_simt(a, bf16, (cudaStream_t)stream);
   if (e == cudaSuccess) e = launch_prefill_simt(a, bf16, (cudaStream_t)stream);
   return cuda_status(e);

@@ -228,6 +228,7 @@ struct PrefillArgs {
   const int32_t* row_count;  // or null
   const void* q;             // [Q][rows][H][dn + dr]
   int64_t q_tok, q_head;
+  int q_vec;                 // every head of q starts on 16 bytes
   const void* w;             // [H][dn + dv][dc]
   void* out;                 // [Q][rows][H][dv]
   void* kv;                  // [cap][H][dn + dv]
@@ -272,6 +273,8 @@ __device__ __forceinline__ int64_t prefill_rows_before(const PrefillArgs& a, int
   return sum;
 }
 
+bool prefill_tc_supported(const PrefillArgs& a, int bf16);
+cudaError_t launch_prefill_tc(const PrefillArgs& a, void* encode_fn, int sms, cudaStream_t s);
 cudaError_t launch_expand_simt(const PrefillArgs& a, int bf16, cudaStream_t s);
 cudaError_t launch_prefill_simt(const PrefillArgs& a, int bf16, cudaStream_t s);
 

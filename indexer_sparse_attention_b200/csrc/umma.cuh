@@ -68,7 +68,7 @@ struct Ctl {
   volatile int* abort_flag;
   ErrWord* err;
 };
-__device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, Ctl c) {
+static __device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, Ctl c) {
   const uint64_t t0 = gtimer();
   for (uint32_t it = 1;; ++it) {
     if (mbar_try(bar, parity)) return true;
