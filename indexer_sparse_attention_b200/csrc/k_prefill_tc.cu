@@ -9,7 +9,7 @@
 //               turns on the tensor cores, one's softmax under the other's
 //               products:
 //   S_t [128 x 128 keys] = Q_t . K^T   M 128, N 128, K 192 (shared memory both)
-//   O_t [128 x 128]     += P_t . V     M 128, N 64 x 2, K 128 (P from TMEM)
+//   O_t [128 x 128]     += P_t . V     M 128, N 128, K 128 (P from TMEM)
 //               P (bf16) overwrites its S in TMEM.  A thread owns a row, so
 //               maximum, sum and rescaling need no exchange; the softmax
 //               reference moves only where a row's maximum has grown by more
@@ -332,14 +332,16 @@ __global__ void __launch_bounds__(kExpThreads, 1)
 // ---------------------------------------------------------------------------
 // attention
 // ---------------------------------------------------------------------------
-constexpr int kAttThreads = 320;  // warps 0..3 and 4..7 the two row tiles' softmax, 8 copies, 9 MMA issue
+constexpr int kAttThreads = 352;  // warps 0..3 and 4..7 the two row tiles' softmax, 8 copies, 9 and 10 MMA issue
 constexpr int kRing = 8;
 constexpr int kKBlocks = 3, kVBlocks = 2, kKV = kKBlocks + kVBlocks;
 
 struct AttMisc {
-  uint64_t full[kRing], empty[kRing];
+  uint64_t kfull[2], vfull[2];  // K(i), V(i) landed: barrier i % 2 (the ring holds less than two key tiles)
+  uint64_t empty[kRing];
   uint64_t qfull[2], sfull[2], pfull[2][2], ofull[2];
-  uint64_t done;
+  uint64_t turn[2];
+  uint64_t done[2];
   int64_t tmp[33];
   uint32_t tmem;
   int abort_flag;
@@ -385,18 +387,18 @@ __global__ void __launch_bounds__(kAttThreads, 1)
 
   if (threadIdx.x == 0) {
     ms.abort_flag = 0;
-    for (int i = 0; i < kRing; ++i) {
-      mbar_init(bar(ms.full[i]), 1);
-      mbar_init(bar(ms.empty[i]), 1);
-    }
+    for (int i = 0; i < kRing; ++i) mbar_init(bar(ms.empty[i]), n1 ? 2 : 1);  // the row tiles' MMA warps
     for (int t = 0; t < 2; ++t) {
+      mbar_init(bar(ms.kfull[t]), 1);
+      mbar_init(bar(ms.vfull[t]), 1);
+      mbar_init(bar(ms.turn[t]), 1);
+      mbar_init(bar(ms.done[t]), 1);
       mbar_init(bar(ms.qfull[t]), 128);
       mbar_init(bar(ms.sfull[t]), 1);
       mbar_init(bar(ms.pfull[t][0]), 4);
       mbar_init(bar(ms.pfull[t][1]), 4);
       mbar_init(bar(ms.ofull[t]), 1);
     }
-    mbar_init(bar(ms.done), 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 9) tmem_alloc(smem_u32(&ms.tmem), 512);
@@ -408,104 +410,132 @@ __global__ void __launch_bounds__(kAttThreads, 1)
 
   if (warp == 8) {
     // ======================= copies =======================
-    uint32_t armed[kRing];
-    for (int i = 0; i < kRing; ++i) armed[i] = 2;
+    uint32_t armed[4] = {2, 2, 2, 2};  // kfull, vfull
     bool ok = true;
     int s = 0;
     uint32_t ph = 0;
     for (int i = 0; i < n && ok; ++i) {
       const int row = (int)(off + (int64_t)i * kRowTile);
+      const uint32_t kf = bar(ms.kfull[i & 1]), vf = bar(ms.vfull[i & 1]), par = (uint32_t)(i >> 1) & 1u;
 #pragma unroll 1
       for (int b = 0; b < kKV; ++b) {
         ok = wait_warp(bar(ms.empty[s]), ph ^ 1u, ctl);
         if (!ok) break;
         if (lane == 0) {
-          mbar_expect_tx(bar(ms.full[s]), kBlk);
+          if (b == 0) mbar_expect_tx(kf, kKBlocks * kBlk);
+          if (b == kKBlocks) mbar_expect_tx(vf, kVBlocks * kBlk);
           if (b == 2)
-            tma_load_2d(r_at + s * kBlk, &map_kr, bar(ms.full[s]), 0, row);
+            tma_load_2d(r_at + s * kBlk, &map_kr, kf, 0, row);
           else
-            tma_load_2d(r_at + s * kBlk, &map_kv, bar(ms.full[s]), h * kN + (b < 2 ? b : b - 1) * 64, row);
+            tma_load_2d(r_at + s * kBlk, &map_kv, b < 2 ? kf : vf, h * kN + (b < 2 ? b : b - 1) * 64, row);
         }
-        armed[s] = ph;
+        if (b == 0) armed[i & 1] = par;
+        if (b == kKBlocks) armed[2 + (i & 1)] = par;
         if (++s == kRing) {
           s = 0;
           ph ^= 1u;
         }
       }
     }
+    // (a group that an abort cut short never completes: its wait ends by its limit)
     if (lane == 0 && ms.abort_flag)
-      for (int i = 0; i < kRing; ++i)
-        if (armed[i] < 2) drain(bar(ms.full[i]), armed[i]);
-  } else if (warp == 9) {
-    // ======================= MMA issue =======================
-    const uint32_t id_s = idesc_bf16(128, 128, 0, 0), id_o = idesc_bf16(128, 64, 0, 1);
-    bool ok = true;
+      for (int i = 0; i < 2; ++i) {
+        if (armed[i] < 2) drain(bar(ms.kfull[i]), armed[i]);
+        if (armed[2 + i] < 2) drain(bar(ms.vfull[i]), armed[2 + i]);
+      }
+  } else if (warp > 8) {
+    // ======================= MMA issue, a warp for each row tile =======================
+    // (One warp for both left the tensor cores idle while it waited: a wait
+    // that succeeds at once takes 75 cycles, and the pipe queues 2 to 4
+    // instructions of 64.)  The products of one tile need their order, those of
+    // the two tiles do not.
+    const int t = warp - 9, nt = t ? n1 : n0;
+    const uint32_t id_s = idesc_bf16(128, 128, 0, 0);
+    const uint32_t id_o = idesc_bf16(128, 128, 0, 1), id_o64 = idesc_bf16(128, 64, 0, 1);
+    const uint32_t s_col = tmem + t * 128, o_col = tmem + kOCol + t * 128;
     // ring blocks of K(i): 5 i .. + 2, of V(i): 5 i + 3, 5 i + 4
-    auto first = [&](int t, int i) {  // S_t(i)
-      const bool last = t == (i < n1 ? 1 : 0);
+    auto k_landed = [&](int i) { return wait_warp(bar(ms.kfull[i & 1]), (uint32_t)(i >> 1) & 1u, ctl); };
+    auto v_landed = [&](int i) { return wait_warp(bar(ms.vfull[i & 1]), (uint32_t)(i >> 1) & 1u, ctl); };
+    auto first = [&](int i) {  // S(i)
+      const int x = kKV * i;
+      uint64_t bd[kKBlocks];
 #pragma unroll
-      for (int b = 0; b < kKBlocks; ++b) {
-        const int x = kKV * i + b, s = x % kRing;
-        ok = ok && wait_warp(bar(ms.full[s]), (uint32_t)(x / kRing) & 1u, ctl);
-        if (!ok) return;
-        fence_after();
-        const uint64_t ad = sw128_desc(q_at + (t * kKBlocks + b) * kBlk, 16, 1024);
-        const uint64_t bd = sw128_desc(r_at + s * kBlk, 16, 1024);
-        if (elect()) {
+      for (int b = 0; b < kKBlocks; ++b) bd[b] = sw128_desc(r_at + (x + b) % kRing * kBlk, 16, 1024);
+      const uint64_t ad = sw128_desc(q_at + t * kKBlocks * kBlk, 16, 1024);
+      fence_after();
+      if (elect()) {
+#pragma unroll
+        for (int b = 0; b < kKBlocks; ++b) {
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
-            mma_f16(tmem + t * 128, ad + 2 * kk, bd + 2 * kk, id_s, b > 0 || kk > 0 ? 1u : 0u);
-          if (last) commit(bar(ms.empty[s]));
-          if (b == kKBlocks - 1) commit(bar(ms.sfull[t]));
+            mma_f16(s_col, ad + b * (kBlk >> 4) + 2 * kk, bd[b] + 2 * kk, id_s, b > 0 || kk > 0 ? 1u : 0u);
+          commit(bar(ms.empty[(x + b) % kRing]));
         }
-        __syncwarp();
+        commit(bar(ms.sfull[t]));
       }
+      __syncwarp();
     };
-    auto second = [&](int t, int i) {  // O_t += P_t(i) V(i)
-      const bool last = t == (i < n1 ? 1 : 0);
+    auto second = [&](int i) -> bool {  // O += P(i) V(i)
+      const int x = kKV * i + kKBlocks, s = x % kRing;
+      const uint64_t bd = sw128_desc(r_at + s * kBlk, kBlk, 1024), be = sw128_desc(r_at, kBlk, 1024);
+      const uint32_t joined = i > 0;
+      // V's two blocks as one operand 128 wide (with N = 64 an instruction takes as long), but where the ring ends
+      // between them
+      const bool split = s == kRing - 1;
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
-        ok = ok && wait_warp(bar(ms.pfull[t][half]), (uint32_t)i & 1u, ctl);
-        if (!ok) return;
+        if (half && !wait_warp(bar(ms.pfull[t][1]), (uint32_t)i & 1u, ctl)) return false;
+        fence_after();
+        if (elect()) {
 #pragma unroll
-        for (int b = 0; b < kVBlocks; ++b) {
-          const int x = kKV * i + kKBlocks + b, s = x % kRing;
-          if (half == 0) ok = ok && wait_warp(bar(ms.full[s]), (uint32_t)(x / kRing) & 1u, ctl);
-          if (!ok) return;
-          fence_after();
-          const uint64_t bd = sw128_desc(r_at + s * kBlk, kBlk, 1024);
-          if (elect()) {
-#pragma unroll
-            for (int kk = 4 * half; kk < 4 * half + 4; ++kk)
-              mma_f16_ts(tmem + kOCol + t * 128 + b * 64, tmem + t * 128 + kk * 8, bd + kk * (2048 >> 4), id_o,
-                         i > 0 || kk > 0 ? 1u : 0u);
-            if (last && half == 1) commit(bar(ms.empty[s]));
+          for (int kk = 4 * half; kk < 4 * half + 4; ++kk) {
+            const uint32_t acc = kk > 0 ? 1u : joined;
+            const uint64_t step = (uint64_t)kk * (2048 >> 4);
+            if (!split) {
+              mma_f16_ts(o_col, s_col + kk * 8, bd + step, id_o, acc);
+            } else {
+              mma_f16_ts(o_col, s_col + kk * 8, bd + step, id_o64, acc);
+              mma_f16_ts(o_col + 64, s_col + kk * 8, be + step, id_o64, acc);
+            }
           }
-          __syncwarp();
+          if (half == 1) {
+            commit(bar(ms.empty[s]));
+            commit(bar(ms.empty[(x + 1) % kRing]));
+            if (i + 1 == nt) commit(bar(ms.ofull[t]));
+          }
         }
-      }
-      if (i + 1 == (t ? n1 : n0)) {
-        if (elect()) commit(bar(ms.ofull[t]));
         __syncwarp();
       }
+      return true;
     };
-#pragma unroll 1
-    for (int t = 0; t < 2; ++t)
-      if (t == 0 || n1) {
-        ok = ok && wait_warp(bar(ms.qfull[t]), 0, ctl);
-        if (ok) first(t, 0);
+    if (nt) {
+      bool ok = wait_warp(bar(ms.qfull[t]), 0, ctl) && k_landed(0);
+      if (ok) first(0);
+      for (int i = 0; ok && i < nt; ++i) {
+        // the tiles take turns, so that one's softmax falls under the other's products (left to themselves they
+        // run in step); what a turn needs is waited for before it
+        ok = v_landed(i) && wait_warp(bar(ms.pfull[t][0]), (uint32_t)i & 1u, ctl);
+        if (ok && n1 && (t ? i < n0 : i > 0))
+          ok = wait_warp(bar(ms.turn[t]), (uint32_t)(t ? i : i - 1) & 1u, ctl);
+        ok = ok && second(i);
+        if (ok && i + 1 < nt) {
+          ok = k_landed(i + 1);  // (not before the turn: the ring has no room for it much earlier)
+          if (ok) first(i + 1);
+        }
+        if (ok && n1 && lane == 0) mbar_arrive(bar(ms.turn[t ^ 1]));
       }
-#pragma unroll 1
-    for (int i = 0; i < n && ok; ++i)
-#pragma unroll 1
-      for (int t = 0; t < 2; ++t) {
-        const int nt = t ? n1 : n0;
-        if (ok && i < nt) second(t, i);
-        if (ok && i + 1 < nt) first(t, i + 1);
-      }
-    if (elect()) commit(bar(ms.done));
+      // The blocks of key tiles that only the other row tile needs: handed
+      // back once they have landed, so that no block is handed back twice in
+      // one round of the ring.
+      if (n1)
+        for (int i = nt; ok && i < n; ++i) {
+          ok = k_landed(i) && v_landed(i);
+          if (ok && lane < kKV) mbar_arrive(bar(ms.empty[(kKV * i + lane) % kRing]));
+        }
+    }
+    if (elect()) commit(bar(ms.done[t]));
     __syncwarp();
-    drain(bar(ms.done), 0);
+    drain(bar(ms.done[t]), 0);
   } else {
     // ======================= softmax and output =======================
     const int t = warp >> 2, tid = threadIdx.x & 127;
