@@ -268,7 +268,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_attn_combine(const __grid_c
 // ---------------------------------------------------------------------------
 constexpr int kES = 32, kEK = 32;  // slots of a block, reduction step
 
-// kv[off + s][h] = W_h c_s for a tile of kES slots and one head; head 0 also
+// kv[h][off + s] = W_h c_s for a tile of kES slots and one head; head 0 also
 // copies the shared key part.  grid (slot tiles, heads, requests).
 template <typename T>
 __global__ void __launch_bounds__(kThreads) k_expand_simt(const __grid_constant__ PrefillArgs a) {
@@ -326,7 +326,7 @@ __global__ void __launch_bounds__(kThreads) k_expand_simt(const __grid_constant_
 #pragma unroll
         for (int s = 0; s < kES; ++s)
           if (s0 + s < ch.end)
-            reinterpret_cast<T*>(a.kv)[((off + s0 + s) * a.H + h) * N + n] = from_f32<T>(acc[c][s]);
+            reinterpret_cast<T*>(a.kv)[(h * a.cap + off + s0 + s) * N + n] = from_f32<T>(acc[c][s]);
     }
     if (h == 0)
       for (int i = threadIdx.x; i < kES * C.dr; i += kThreads) {
@@ -382,7 +382,7 @@ __global__ void __launch_bounds__(kThreads) k_prefill_simt(const __grid_constant
         float v = 0.f;
         if (j0 + j < ch.end) {
           const int64_t s = off + j0 + j;
-          const T* kv = reinterpret_cast<const T*>(a.kv) + (s * a.H + h) * N;
+          const T* kv = reinterpret_cast<const T*>(a.kv) + (h * a.cap + s) * N;
           v = to_f32(d < a.dn ? kv[d] : d < W ? reinterpret_cast<const T*>(a.kr)[s * dr + d - a.dn] : kv[d - dr]);
         }
         t.kv[j * t.stride + d] = v;

@@ -312,7 +312,7 @@ __global__ void __launch_bounds__(kExpThreads, 1)
         if (threadIdx.x == 0) {
           asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
                            (uint64_t)&map_kv),
-                       "r"(o_at + buf * kBlk), "r"(w.h * kN + c * 64), "r"((int)(w.off + w.tile * kSlotTile))
+                       "r"(o_at + buf * kBlk), "r"(c * 64), "r"((int)(w.h * a.cap + w.off + w.tile * kSlotTile))
                        : "memory");
           asm volatile("cp.async.bulk.commit_group;" ::: "memory");
         }
@@ -427,7 +427,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
           if (b == 2)
             tma_load_2d(r_at + s * kBlk, &map_kr, kf, 0, row);
           else
-            tma_load_2d(r_at + s * kBlk, &map_kv, b < 2 ? kf : vf, h * kN + (b < 2 ? b : b - 1) * 64, row);
+            tma_load_2d(r_at + s * kBlk, &map_kv, b < 2 ? kf : vf, (b < 2 ? b : b - 1) * 64, (int)(h * a.cap) + row);
         }
         if (b == 0) armed[i & 1] = par;
         if (b == kKBlocks) armed[2 + (i & 1)] = par;
@@ -685,7 +685,7 @@ cudaError_t launch_prefill_tc(const PrefillArgs& a, void* encode_fn, int sms, cu
   const uint32_t box = (uint32_t)(a.cache.b < kSlotTile ? a.cache.b : kSlotTile);
   if (!encode_rows(encode_fn, &mc, a.cache.data, rows, kDC + kDR, (kDC + kDR) * 2, box) ||
       !encode_rows(encode_fn, &mw, a.w, (uint64_t)a.H * kN, kDC, kDC * 2, kN) ||
-      !encode_rows(encode_fn, &mkv, a.kv, (uint64_t)a.cap, (uint64_t)a.H * kN, (uint64_t)a.H * kN * 2, kRowTile) ||
+      !encode_rows(encode_fn, &mkv, a.kv, (uint64_t)a.H * a.cap, kN, kN * 2, kRowTile) ||
       !encode_rows(encode_fn, &mkr, a.kr, (uint64_t)a.cap, kDR, kDR * 2, kRowTile))
     return cudaErrorInvalidValue;
   cudaError_t e = cudaFuncSetAttribute(k_expand_tc, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kExpSmem);

@@ -231,7 +231,7 @@ struct PrefillArgs {
   int q_vec;                 // every head of q starts on 16 bytes
   const void* w;             // [H][dn + dv][dc]
   void* out;                 // [Q][rows][H][dv]
-  void* kv;                  // [cap][H][dn + dv]
+  void* kv;                  // [H][cap][dn + dv]
   void* kr;                  // [cap][dr]
   float scale_log2;
   ErrWord* err;
