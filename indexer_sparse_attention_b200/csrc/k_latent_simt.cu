@@ -402,19 +402,35 @@ __global__ void __launch_bounds__(kThreads) k_prefill_simt(const __grid_constant
   }
 }
 
-template <typename F>
-cudaError_t with_smem(F kernel, size_t smem) {
-  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+// Shared memory of a block; the largest dims take less than kMaxSmem.
+constexpr int kMaxSmem = 160 * 1024;
+size_t attn_smem(int W) {
+  return sizeof(float) * (kNH * W + kT * (W + 1) + kNH * kT + kNH + 2) + sizeof(int64_t) * kT;
+}
+size_t expand_smem(int N) { return sizeof(float) * (kEK * (kES + 1) + (size_t)N * (kEK + 1)); }
+size_t prefill_smem(int W, int dv) { return sizeof(float) * (kNH * W + kT * ((W + dv) | 1) + kNH * kT + kNH); }
+
+template <typename T>
+cudaError_t raise_limits() {
+  cudaError_t e = cudaFuncSetAttribute(k_attn_simt<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(k_expand_simt<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(k_prefill_simt<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+  return e;
 }
 
 }  // namespace
 
+cudaError_t prepare_attn_simt() {
+  const cudaError_t e = raise_limits<float>();
+  return e == cudaSuccess ? raise_limits<__nv_bfloat16>() : e;
+}
+
 cudaError_t launch_attn_simt(const AttnArgs& a, int bf16, cudaStream_t s) {
   const int W = a.cache.dc + a.cache.dr;
-  const size_t smem = sizeof(float) * (kNH * W + kT * (W + 1) + kNH * kT + kNH + 2) + sizeof(int64_t) * kT;
+  const size_t smem = attn_smem(W);
   auto kernel = bf16 ? k_attn_simt<__nv_bfloat16> : k_attn_simt<float>;
-  cudaError_t e = with_smem(kernel, smem);
-  if (e != cudaSuccess) return e;
   PdlLaunch l(dim3((unsigned)(a.ranges * a.ngroups)), dim3(kThreads), smem, s);
   return cudaLaunchKernelEx(&l.cfg, kernel, a);
 }
@@ -431,10 +447,8 @@ cudaError_t launch_attn_combine(const AttnArgs& a, int bf16, cudaStream_t s) {
 }
 
 cudaError_t launch_expand_simt(const PrefillArgs& a, int bf16, cudaStream_t s) {
-  const size_t smem = sizeof(float) * (kEK * (kES + 1) + (size_t)(a.dn + a.dv) * (kEK + 1));
+  const size_t smem = expand_smem(a.dn + a.dv);
   auto kernel = bf16 ? k_expand_simt<__nv_bfloat16> : k_expand_simt<float>;
-  cudaError_t e = with_smem(kernel, smem);
-  if (e != cudaSuccess) return e;
   const int64_t tiles = ((int64_t)a.max_slots + kES - 1) / kES;
   PdlLaunch l(dim3((unsigned)(tiles < 1024 ? tiles : 1024), (unsigned)a.H, (unsigned)a.Q), dim3(kThreads), smem, s);
   return cudaLaunchKernelEx(&l.cfg, kernel, a);
@@ -442,10 +456,8 @@ cudaError_t launch_expand_simt(const PrefillArgs& a, int bf16, cudaStream_t s) {
 
 cudaError_t launch_prefill_simt(const PrefillArgs& a, int bf16, cudaStream_t s) {
   const int W = a.dn + a.cache.dr;
-  const size_t smem = sizeof(float) * (kNH * W + kT * ((W + a.dv) | 1) + kNH * kT + kNH);
+  const size_t smem = prefill_smem(W, a.dv);
   auto kernel = bf16 ? k_prefill_simt<__nv_bfloat16> : k_prefill_simt<float>;
-  cudaError_t e = with_smem(kernel, smem);
-  if (e != cudaSuccess) return e;
   const int64_t tiles = ((int64_t)a.rows + kNH - 1) / kNH;
   PdlLaunch l(dim3((unsigned)(tiles < 4096 ? tiles : 4096), (unsigned)a.H, (unsigned)a.Q), dim3(kThreads), smem, s);
   return cudaLaunchKernelEx(&l.cfg, kernel, a);

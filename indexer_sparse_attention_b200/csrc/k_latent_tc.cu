@@ -690,11 +690,12 @@ bool attn_tc_supported(const AttnArgs& a, int bf16) {
          ((int64_t)a.cache.num_pages << a.cache.log2b) < (int64_t(1) << 31) && ((uintptr_t)a.out & 15) == 0;
 }
 
+cudaError_t prepare_attn_tc() {
+  return cudaFuncSetAttribute(k_attn_tc, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_bytes(kTcHeads));
+}
+
 cudaError_t launch_attn_tc(const AttnArgs& a, cudaStream_t s) {
-  const uint32_t smem = smem_bytes(a.group);
-  cudaError_t e = cudaFuncSetAttribute(k_attn_tc, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e != cudaSuccess) return e;
-  PdlLaunch l(dim3((unsigned)(a.ranges * a.ngroups)), dim3(kThreads), smem, s);
+  PdlLaunch l(dim3((unsigned)(a.ranges * a.ngroups)), dim3(kThreads), smem_bytes(a.group), s);
   return cudaLaunchKernelEx(&l.cfg, k_attn_tc, a);
 }
 

@@ -679,6 +679,13 @@ bool prefill_tc_supported(const PrefillArgs& a, int bf16) {
          a.cap * a.H < (int64_t(1) << 31);
 }
 
+cudaError_t prepare_prefill_tc() {
+  const cudaError_t e = cudaFuncSetAttribute(k_expand_tc, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kExpSmem);
+  return e == cudaSuccess
+             ? cudaFuncSetAttribute(k_prefill_tc, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kAttSmem)
+             : e;
+}
+
 cudaError_t launch_prefill_tc(const PrefillArgs& a, void* encode_fn, int sms, cudaStream_t s) {
   CUtensorMap mc, mw, mkv, mkr;
   const uint64_t rows = (uint64_t)a.cache.num_pages << a.cache.log2b;
@@ -688,10 +695,7 @@ cudaError_t launch_prefill_tc(const PrefillArgs& a, void* encode_fn, int sms, cu
       !encode_rows(encode_fn, &mkv, a.kv, (uint64_t)a.H * a.cap, kN, kN * 2, kRowTile) ||
       !encode_rows(encode_fn, &mkr, a.kr, (uint64_t)a.cap, kDR, kDR * 2, kRowTile))
     return cudaErrorInvalidValue;
-  cudaError_t e = cudaFuncSetAttribute(k_expand_tc, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kExpSmem);
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(k_prefill_tc, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kAttSmem);
-  if (e != cudaSuccess) return e;
+  cudaError_t e;
   {
     PdlLaunch l(dim3((unsigned)sms), dim3(kExpThreads), kExpSmem, s);
     e = cudaLaunchKernelEx(&l.cfg, k_expand_tc, a, mc, mw, mkv);

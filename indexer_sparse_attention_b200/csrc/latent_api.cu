@@ -86,7 +86,7 @@ bool valid_config(const spin_latent_config* c) {
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 struct Carve {
-  size_t err, ml, part, kv, kr, total;
+  size_t err, turn, ml, part, kv, kr, total;
 };
 
 Carve carve(const spin_latent_config* c) {
@@ -104,6 +104,7 @@ Carve carve(const spin_latent_config* c) {
   const int group = std::min(kTcHeads, (c->num_heads + 15) / 16 * 16);
   const size_t heads = std::max<size_t>((size_t)2 * kTcBlocks * group, (size_t)2 * kSimtBlocks * kSimtHeads);
   k.err = take(sizeof(ErrWord));
+  k.turn = take(kMaxRopeDim / 2 * sizeof(uint64_t));
   k.ml = take(heads * sizeof(float2));
   k.part = take(heads * c->latent_dim * sizeof(float));
   k.kv = take(c->prefill_slots ? (size_t)c->prefill_slots * c->num_heads * (c->nope_dim + c->v_dim) * el : 0);
@@ -114,8 +115,12 @@ Carve carve(const spin_latent_config* c) {
 
 // f_i of every pair in double (arXiv 2309.00071 for YaRN), as the fraction of
 // a turn per position in units of 2^-64.
-RopeTable rope_table(const spin_latent_config& c) {
-  RopeTable t{};
+struct RopeValues {
+  uint64_t turn[kMaxRopeDim / 2];
+  float mul;
+};
+RopeValues rope_values(const spin_latent_config& c) {
+  RopeValues t{};
   const int d = c.rope_dim;
   const double two_pi = 6.283185307179586476925286766559;
   t.mul = 1.0f;
@@ -194,7 +199,9 @@ spin_status spin_latent_create(const spin_latent_config* cfg, void* dev_mem, siz
   lt->part = (float*)(lt->base + k.part);
   lt->kv = lt->base + k.kv;
   lt->kr = lt->base + k.kr;
-  lt->rope = rope_table(*cfg);
+  const RopeValues rope = rope_values(*cfg);
+  lt->rope.turn = (const uint64_t*)(lt->base + k.turn);
+  lt->rope.mul = rope.mul;
   lt->sms = kTcBlocks;
   cudaDeviceGetAttribute(&lt->sms, cudaDevAttrMultiProcessorCount, at.device);
   cudaDriverEntryPointQueryResult qres;
@@ -204,6 +211,12 @@ spin_status spin_latent_create(const spin_latent_config* cfg, void* dev_mem, siz
     lt->encode_fn = fn;
   cudaGetLastError();
   e = cudaMemsetAsync(lt->err, 0, sizeof(ErrWord), (cudaStream_t)stream);
+  // (from pageable memory: copied out of `rope` before the call returns)
+  if (e == cudaSuccess)
+    e = cudaMemcpyAsync(lt->base + k.turn, rope.turn, sizeof(rope.turn), cudaMemcpyHostToDevice, (cudaStream_t)stream);
+  if (e == cudaSuccess) e = prepare_attn_tc();
+  if (e == cudaSuccess) e = prepare_attn_simt();
+  if (e == cudaSuccess) e = prepare_prefill_tc();
   if (e != cudaSuccess) {
     delete lt;
     return cuda_status(e);

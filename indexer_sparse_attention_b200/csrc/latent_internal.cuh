@@ -17,8 +17,8 @@ namespace spin {
 // ---------------------------------------------------------------------------
 constexpr int kMaxRopeDim = 128;
 struct RopeTable {
-  uint64_t turn[kMaxRopeDim / 2];
-  float mul;  // on cos and sin
+  const uint64_t* turn;  // [rope_dim / 2] in device memory (each thread reads another pair's)
+  float mul;             // on cos and sin
 };
 
 // cos and sin of a position, scaled.  The fraction's top 32 bits, read as a
@@ -42,13 +42,6 @@ template <>
 __device__ __forceinline__ float from_f32<float>(float x) { return x; }
 template <>
 __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
-
-// 16 bytes of elements, as floats and back (each rounded once to T).
-template <typename T>
-struct Vec16 {
-  static constexpr int kN = 16 / (int)sizeof(T);
-  T v[kN];
-};
 
 struct RopeArgs {
   RopeTable tab;
@@ -207,6 +200,11 @@ constexpr int kSimtHeads = 8, kSimtTile = 32, kSimtBlocks = 296;
 // Heads, tokens and grid limit of the tensor-core kernel (one block per SM).
 constexpr int kTcHeads = 64, kTcTile = 64, kTcBlocks = 148;
 
+// The prepare_ calls raise the kernels' shared-memory limits on the current
+// device, once for each handle.
+cudaError_t prepare_attn_simt();
+cudaError_t prepare_attn_tc();
+cudaError_t prepare_prefill_tc();
 cudaError_t launch_attn_simt(const AttnArgs& a, int bf16, cudaStream_t s);
 bool attn_tc_supported(const AttnArgs& a, int bf16);
 cudaError_t launch_attn_tc(const AttnArgs& a, cudaStream_t s);

@@ -10,6 +10,7 @@ stream, whichever device is current; all tensors must live there.
 from __future__ import annotations
 
 import ctypes
+import sys
 from typing import Optional
 
 import torch
@@ -52,8 +53,8 @@ SIGNATURES = {
 
 
 def _pkg():
-    import indexer_sparse_attention_b200 as isa
-    return isa
+    """The package itself (it imports this module, so not at the top)."""
+    return sys.modules[__package__]
 
 
 def make_latent_config(*, num_requests, max_slots, block_size=64, num_heads=128, latent_dim=512, rope_dim=64,
@@ -110,49 +111,49 @@ class SpinLatent:
             pass
 
 
-def _stream(lt: SpinLatent, stream) -> _vp:
+def _stream(lt: SpinLatent, stream) -> int:
     if stream is None:
-        stream = torch.cuda.current_stream(lt.device)
-    elif stream.device != lt.device:
+        return torch._C._cuda_getCurrentRawStream(lt.device.index)
+    if stream.device != lt.device:
         raise ValueError(f"the stream is on {stream.device}, the handle on {lt.device}")
-    return _vp(stream.cuda_stream)
+    return stream.cuda_stream
 
 
 def _place(lt: SpinLatent, t: torch.Tensor, name: str, dtype) -> None:
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
     if t.device != lt.device:
         raise ValueError(f"{name} must be on {lt.device}, got {t.device}")
-    if t.dtype != dtype:
-        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
 
 
-def _dense(lt: SpinLatent, t: Optional[torch.Tensor], name: str, dtype, shape) -> _vp:
-    """A contiguous tensor of exactly this shape (None: a NULL pointer)."""
+def _dense(lt: SpinLatent, t: Optional[torch.Tensor], name: str, dtype, shape: tuple) -> Optional[int]:
+    """The address of a contiguous tensor of exactly this shape (None: a NULL pointer)."""
     if t is None:
-        return _vp(0)
+        return None
     _place(lt, t, name, dtype)
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must have the shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have the shape {shape}, got {tuple(t.shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    return _vp(t.data_ptr())
+    return t.data_ptr()
 
 
-def _stride(t: torch.Tensor, dim: int) -> int:
-    return t.stride(dim) if t.shape[dim] > 1 else 0
-
-
-def _tokens(lt: SpinLatent, t: torch.Tensor, name: str, shape):
-    """(pointer, token stride, head stride) of a tensor [Q, rows, (heads,) width] whose tokens lie at one stride."""
+def _tokens(lt: SpinLatent, t: torch.Tensor, name: str, shape: tuple):
+    """(address, token stride, head stride) of a tensor [Q, rows, (heads,) width] whose tokens lie at one stride."""
     _place(lt, t, name, lt.dtype)
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must have the shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.stride(-1) != 1:
+    if t.shape != shape:
+        raise ValueError(f"{name} must have the shape {shape}, got {tuple(t.shape)}")
+    st = t.stride()
+    if st[-1] != 1:
         raise ValueError(f"the last dimension of {name} must be contiguous")
-    Q, rows = t.shape[:2]
-    if Q > 1 and rows > 1 and t.stride(0) != rows * t.stride(1):
-        raise ValueError(f"the rows of all requests of {name} must lie at one stride")
-    token = _stride(t, 1) if rows > 1 else _stride(t, 0)
-    return _vp(t.data_ptr()), token, _stride(t, 2) if t.dim() == 4 else 0
+    Q, rows = shape[:2]
+    if rows > 1:
+        if Q > 1 and st[0] != rows * st[1]:
+            raise ValueError(f"the rows of all requests of {name} must lie at one stride")
+        token = st[1]
+    else:
+        token = st[0] if Q > 1 else 0
+    return t.data_ptr(), token, st[2] if len(shape) == 4 and shape[2] > 1 else 0
 
 
 def _cache(lt: SpinLatent, cache: torch.Tensor, block_table: torch.Tensor):
@@ -161,13 +162,12 @@ def _cache(lt: SpinLatent, cache: torch.Tensor, block_table: torch.Tensor):
         raise ValueError("cache must have the shape (pages, block_size, latent_dim + rope_dim)")
     if block_table.dim() != 2:
         raise ValueError("block_table must have the shape (num_requests, blocks)")
+    pages, columns = cache.shape[0], block_table.shape[1]
     blocks = -(-c.max_slots // c.block_size)
-    if block_table.shape[1] < blocks:
-        raise ValueError(f"block_table must have at least {blocks} columns, got {block_table.shape[1]}")
-    return (_dense(lt, cache, "cache", lt.dtype, (cache.shape[0], c.block_size, c.latent_dim + c.rope_dim)),
-            cache.shape[0],
-            _dense(lt, block_table, "block_table", torch.int32, (c.num_requests, block_table.shape[1])),
-            block_table.shape[1])
+    if columns < blocks:
+        raise ValueError(f"block_table must have at least {blocks} columns, got {columns}")
+    return (_dense(lt, cache, "cache", lt.dtype, (pages, c.block_size, c.latent_dim + c.rope_dim)), pages,
+            _dense(lt, block_table, "block_table", torch.int32, (c.num_requests, columns)), columns)
 
 
 def _overlap(a: torch.Tensor, b: torch.Tensor) -> bool:
@@ -182,28 +182,42 @@ def _overlap(a: torch.Tensor, b: torch.Tensor) -> bool:
 # --------------------------------------------------------------------------
 # entry points (same names as the C ABI)
 # --------------------------------------------------------------------------
+def _call(name: str, *args) -> None:
+    status = getattr(_pkg().load(), name)(*args)
+    if status != 0:
+        raise _pkg().SpinError(status, name)
+
+
 def spin_rope(lt: SpinLatent, x: torch.Tensor, positions: torch.Tensor, offset: int = 0,
               out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """Rotates elements offset .. offset + rope_dim - 1 of every head of x
     [tokens, heads, head_dim] by its token's position; ``out`` None: in place.
     Returns the tensor it wrote."""
-    isa = _pkg()
     out = x if out is None else out
-    if x.dim() != 3 or out.shape != x.shape:
+    shape = x.shape
+    if len(shape) != 3 or out.shape != shape:
         raise ValueError("x and out must have one shape (tokens, heads, head_dim)")
-    for t, name in ((x, "x"), (out, "out")):
-        _place(lt, t, name, lt.dtype)
-        if t.stride(-1) != 1:
-            raise ValueError(f"the last dimension of {name} must be contiguous")
-    if any(n > 1 and s < w for n, s, w in ((x.shape[0], out.stride(0), 1), (x.shape[1], out.stride(1), x.shape[2]))):
+    _place(lt, x, "x", lt.dtype)
+    tokens, heads, width = shape
+    sx = x.stride()
+    xt, xh = sx[0] if tokens > 1 else 0, sx[1] if heads > 1 else 0
+    if out is x:
+        so, ot, oh = sx, xt, xh
+    else:
+        _place(lt, out, "out", lt.dtype)
+        so = out.stride()
+        ot, oh = so[0] if tokens > 1 else 0, so[1] if heads > 1 else 0
+    if sx[2] != 1 or so[2] != 1:
+        raise ValueError("the last dimension of x and out must be contiguous")
+    # heads of out one behind the other in either order: the inner ones do not reach the next outer one
+    lo, hi = sorted((s, n) for s, n in ((ot, tokens), (oh, heads)) if n > 1) if tokens > 1 < heads else \
+        ((max(ot, oh), 1), (max(ot, oh), max(tokens, heads)))
+    if (lo[1] > 1 and lo[0] < width) or (hi[1] > 1 and hi[0] < lo[0] * (lo[1] - 1) + width):
         raise ValueError("the heads of out must not overlap")
-    same = out.data_ptr() == x.data_ptr() and all(_stride(out, d) == _stride(x, d) for d in (0, 1))
-    if not same and _overlap(x, out):
+    if out is not x and (out.data_ptr() != x.data_ptr() or ot != xt or oh != xh) and _overlap(x, out):
         raise ValueError("out must be x or not overlap it")
-    pos = _dense(lt, positions, "positions", torch.int32, x.shape[:1])
-    isa._check(isa.load().spin_rope(lt.handle, x.shape[0], x.shape[1], x.shape[2], offset, _vp(x.data_ptr()),
-                                    _stride(x, 0), _stride(x, 1), pos, _vp(out.data_ptr()), _stride(out, 0),
-                                    _stride(out, 1), _stream(lt, stream)), "spin_rope")
+    _call("spin_rope", lt.handle, tokens, heads, width, offset, x.data_ptr(), xt, xh,
+          _dense(lt, positions, "positions", torch.int32, (tokens,)), out.data_ptr(), ot, oh, _stream(lt, stream))
     return out
 
 
@@ -212,15 +226,13 @@ def spin_latent_append(lt: SpinLatent, rows: int, c: torch.Tensor, k_rope: torch
                        stream=None) -> None:
     """Writes c [Q, rows, latent_dim] and the rotated k_rope [Q, rows,
     rope_dim] into slots ctx_len - 1 .. of each request."""
-    isa = _pkg()
     cfg = lt.cfg
     Q = cfg.num_requests
     cp, ct, _ = _tokens(lt, c, "c", (Q, rows, cfg.latent_dim))
     kp, kt, _ = _tokens(lt, k_rope, "k_rope", (Q, rows, cfg.rope_dim))
-    isa._check(isa.load().spin_latent_append(
-        lt.handle, rows, cp, ct, kp, kt, *_cache(lt, cache, block_table),
-        _dense(lt, ctx_len, "ctx_len", torch.int32, (Q,)), _dense(lt, row_count, "row_count", torch.int32, (Q,)),
-        _stream(lt, stream)), "spin_latent_append")
+    _call("spin_latent_append", lt.handle, rows, cp, ct, kp, kt, *_cache(lt, cache, block_table),
+          _dense(lt, ctx_len, "ctx_len", torch.int32, (Q,)), _dense(lt, row_count, "row_count", torch.int32, (Q,)),
+          _stream(lt, stream))
 
 
 def spin_latent_attention(lt: SpinLatent, rows: int, cache: torch.Tensor, block_table: torch.Tensor,
@@ -230,16 +242,15 @@ def spin_latent_attention(lt: SpinLatent, rows: int, cache: torch.Tensor, block_
     """Absorbed attention of q_latent [Q, rows, H, latent_dim], q_rope [Q,
     rows, H, rope_dim] over the slots that topk [Q, rows, k] lists (None: all
     visible ones) into out [Q, rows, H, latent_dim] and lse [Q, rows, H]."""
-    isa = _pkg()
     cfg = lt.cfg
     Q, H = cfg.num_requests, cfg.num_heads
     ql = _tokens(lt, q_latent, "q_latent", (Q, rows, H, cfg.latent_dim))
     qr = _tokens(lt, q_rope, "q_rope", (Q, rows, H, cfg.rope_dim))
-    isa._check(isa.load().spin_latent_attention(
-        lt.handle, rows, *_cache(lt, cache, block_table), *ql, *qr,
-        _dense(lt, ctx_len, "ctx_len", torch.int32, (Q,)), _dense(lt, topk, "topk", torch.int32, (Q, rows, cfg.topk)),
-        _dense(lt, out, "out", lt.dtype, (Q, rows, H, cfg.latent_dim)),
-        _dense(lt, lse, "lse", torch.float32, (Q, rows, H)), _stream(lt, stream)), "spin_latent_attention")
+    _call("spin_latent_attention", lt.handle, rows, *_cache(lt, cache, block_table), *ql, *qr,
+          _dense(lt, ctx_len, "ctx_len", torch.int32, (Q,)),
+          _dense(lt, topk, "topk", torch.int32, (Q, rows, cfg.topk)),
+          _dense(lt, out, "out", lt.dtype, (Q, rows, H, cfg.latent_dim)),
+          _dense(lt, lse, "lse", torch.float32, (Q, rows, H)), _stream(lt, stream))
 
 
 def spin_latent_prefill(lt: SpinLatent, rows: int, cache: torch.Tensor, block_table: torch.Tensor, q: torch.Tensor,
@@ -247,17 +258,15 @@ def spin_latent_prefill(lt: SpinLatent, rows: int, cache: torch.Tensor, block_ta
                         out: torch.Tensor, stream=None) -> None:
     """Expanded attention of a chunk q [Q, rows, H, nope_dim + rope_dim] over
     the context its tokens were appended to, into out [Q, rows, H, v_dim]."""
-    isa = _pkg()
     cfg = lt.cfg
     Q, H = cfg.num_requests, cfg.num_heads
     if not cfg.prefill_slots:
-        raise isa.SpinError(7, "spin_latent_prefill (the handle has no prefill_slots)")
+        raise _pkg().SpinError(7, "spin_latent_prefill (the handle has no prefill_slots)")
     qp = _tokens(lt, q, "q", (Q, rows, H, cfg.nope_dim + cfg.rope_dim))
-    isa._check(isa.load().spin_latent_prefill(
-        lt.handle, rows, *_cache(lt, cache, block_table), *qp,
-        _dense(lt, w_kv, "w_kv", lt.dtype, (H, cfg.nope_dim + cfg.v_dim, cfg.latent_dim)),
-        _dense(lt, ctx_len, "ctx_len", torch.int32, (Q,)), _dense(lt, row_count, "row_count", torch.int32, (Q,)),
-        _dense(lt, out, "out", lt.dtype, (Q, rows, H, cfg.v_dim)), _stream(lt, stream)), "spin_latent_prefill")
+    _call("spin_latent_prefill", lt.handle, rows, *_cache(lt, cache, block_table), *qp,
+          _dense(lt, w_kv, "w_kv", lt.dtype, (H, cfg.nope_dim + cfg.v_dim, cfg.latent_dim)),
+          _dense(lt, ctx_len, "ctx_len", torch.int32, (Q,)), _dense(lt, row_count, "row_count", torch.int32, (Q,)),
+          _dense(lt, out, "out", lt.dtype, (Q, rows, H, cfg.v_dim)), _stream(lt, stream))
 
 
 def spin_latent_error(lt: SpinLatent, stream=None):

@@ -40,7 +40,7 @@ def handle(Q, max_slots, *, poison=True, **over):
     over.setdefault("softmax_scale", 0.0722)
     lt = isa.SpinLatent(isa.make_latent_config(num_requests=Q, max_slots=max_slots, **over))
     if poison:
-        lt.base[256:] = 255
+        lt.base[768:] = 255  # behind the error word and the rotary frequencies
     return lt
 
 
@@ -439,7 +439,7 @@ def test_attention_without_lse_on_another_stream_and_in_a_graph(dtype, H):
     ctx.copy_(ints([800, 101, 2]))
     topk.copy_(lists_for(gen(9), [800, 101, 2], 1, 300))
     cache.copy_(randn(gen(10), *cache.shape, dtype=dtype))
-    lt.base[256:] = 255
+    lt.base[768:] = 255
     graph.replay()
     want, _ = run_attention(lt, 1, cache, bt, ql, qr, ctx, topk)
     assert torch.equal(cap, want)
@@ -561,7 +561,7 @@ def test_prefill_takes_strided_and_unaligned_queries_and_graphs():
     graph, cap = torch.cuda.CUDAGraph(), torch.full_like(out, 7)
     with torch.cuda.graph(graph):
         isa.spin_latent_prefill(lt, 140, cache, bt, qv, w, ctx, count, cap)
-    lt.base[256:] = 255
+    lt.base[768:] = 255
     graph.replay()
     assert torch.equal(cap, out)
     ctx.copy_(ints([30, 1]))
