@@ -16,6 +16,8 @@
 //               than 8 (log2 units), and then its warp rescales O.  K and V come
 //               as 16 KB blocks of 64 columns through one ring of eight, in the
 //               order of use.
+#include <algorithm>
+
 #include "latent_internal.cuh"
 #include "umma.cuh"
 
@@ -336,6 +338,61 @@ constexpr int kAttThreads = 352;  // warps 0..3 and 4..7 the two row tiles' soft
 constexpr int kRing = 8;
 constexpr int kKBlocks = 3, kVBlocks = 2, kKV = kKBlocks + kVBlocks;
 
+// Which rows of which head a block takes.  A class is 256 rows of a request.
+// The classes are ranked by their key tiles, longest first, and the units
+// (class, head) go to the blocks in that order, so that what starts last is
+// short.  The units behind the last full round of kTail blocks are cut along the
+// keys into as many parts as fill the round, each part's maximum, sum and
+// unnormalised output left in the workspace for the join (a chunk of few rows
+// on a long context is cut into up to kMaxParts).
+constexpr int kTail = 148, kMaxParts = 16, kPlanClasses = 256, kMinPart = 4;
+struct Plan {
+  int order[kPlanClasses];  // classes by rank; the empty ones last
+  int tiles[kPlanClasses];  // key tiles by class
+  int used;                 // classes that are not empty
+};
+struct Unit {
+  int q, r0, h;
+  int part, parts;
+  int slot;  // of the parts in the workspace
+};
+
+// All threads of the block (a multiple of 32 threads).
+__device__ __forceinline__ void make_plan(const PrefillArgs& a, Plan& p) {
+  const int per = (a.rows + 2 * kRowTile - 1) / (2 * kRowTile), classes = a.Q * per;
+  if (threadIdx.x == 0) p.used = 0;
+  __syncthreads();
+  for (int c = threadIdx.x; c < classes; c += blockDim.x) {
+    const int q = c / per, r0 = (c - q * per) * 2 * kRowTile;
+    const Chunk ch = prefill_chunk(a, q, false);
+    int64_t off = 0;
+    for (int i = 0; i < q; ++i) off += (prefill_chunk(a, i, false).end + kSlotTile - 1) / kSlotTile * kSlotTile;
+    const bool any = r0 < ch.count && off + ch.end <= a.cap;
+    p.tiles[c] = any ? (ch.ctx - 2 + min(ch.count, r0 + 2 * kRowTile)) / kRowTile + 1 : 0;
+    if (any) atomicAdd(&p.used, 1);
+  }
+  __syncthreads();
+  for (int c = threadIdx.x; c < classes; c += blockDim.x) {
+    const int n = p.tiles[c];
+    int rank = 0;
+    for (int i = 0; i < classes; ++i) rank += p.tiles[i] > n || (p.tiles[i] == n && i < c);
+    p.order[rank] = c;
+  }
+  __syncthreads();
+}
+// Unit u of the ranked ones.
+__device__ __forceinline__ Unit unit_at(const PrefillArgs& a, const Plan& p, int u) {
+  const int per = (a.rows + 2 * kRowTile - 1) / (2 * kRowTile);
+  // one request: head by head, so that a head's keys are read by its rows at once
+  const int c = p.order[a.Q == 1 ? u % p.used : u / a.H];
+  return {c / per, c % per * 2 * kRowTile, a.Q == 1 ? u / p.used : u % a.H, 0, 1, 0};
+}
+// The tail's units, and the parts of one with n key tiles.
+__device__ __forceinline__ int tail_of(const PrefillArgs& a, const Plan& p) { return p.used * a.H % kTail; }
+__device__ __forceinline__ int parts_of(int tail, int n) {
+  return max(1, min(min(kTail / tail, kMaxParts), n / kMinPart));
+}
+
 struct AttMisc {
   uint64_t kfull[2], vfull[2];  // K(i), V(i) landed: barrier i % 2 (the ring holds less than two key tiles)
   uint64_t empty[kRing];
@@ -361,10 +418,35 @@ __global__ void __launch_bounds__(kAttThreads, 1)
   auto bar = [](uint64_t& b) { return smem_u32(&b); };
   const Ctl ctl{&ms.abort_flag, a.err};
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int h = blockIdx.y, q = blockIdx.z;
-  const int r0 = (gridDim.x - 1 - blockIdx.x) * 2 * kRowTile;  // the longest rows first
 
   pdl_enter();
+  Unit w;
+  if (a.planned) {
+    Plan& p = *reinterpret_cast<Plan*>(r_sm);  // (the ring is not in use yet)
+    make_plan(a, p);
+    const int units = p.used * a.H, tail = tail_of(a, p), whole = units - tail;
+    int u = blockIdx.x;
+    if (u >= whole) {
+      if (!tail) return;
+      const int most = min(kTail / tail, kMaxParts), x = u - whole;
+      u = whole + x / most;
+      if (u >= units) return;
+      w = unit_at(a, p, u);
+      w.part = x % most;
+      w.parts = parts_of(tail, p.tiles[p.order[a.Q == 1 ? u % p.used : u / a.H]]);
+      w.slot = x;
+      if (w.part >= w.parts) return;
+    } else {
+      w = unit_at(a, p, u);
+    }
+    fence_async_smem();  // the plan has been read; copies through the async proxy take its place
+    __syncthreads();
+  } else {
+    const int per = (a.rows + 2 * kRowTile - 1) / (2 * kRowTile);
+    const int c = blockIdx.x / a.H;
+    w = {c / per, (per - 1 - c % per) * 2 * kRowTile, (int)blockIdx.x % a.H, 0, 1, 0};
+  }
+  const int h = w.h, q = w.q, r0 = w.r0;
   const Chunk ch = prefill_chunk(a, q, false);
   if (r0 >= ch.count) return;
   const int64_t off = prefill_rows_before(a, q, ms.tmp);
@@ -381,13 +463,16 @@ __global__ void __launch_bounds__(kAttThreads, 1)
   // rows and key tiles of the two row tiles
   const int rows0 = min(ch.count - r0, kRowTile), rows1 = max(0, min(ch.count - r0 - kRowTile, kRowTile));
   const int pos0 = ch.ctx - 1 + r0;  // of the first row
-  const int n0 = (pos0 + rows0 - 1) / kRowTile + 1;
-  const int n1 = rows1 ? (pos0 + kRowTile + rows1 - 1) / kRowTile + 1 : 0;
-  const int n = max(n0, n1);
+  const int all0 = (pos0 + rows0 - 1) / kRowTile + 1, all1 = rows1 ? (pos0 + kRowTile + rows1 - 1) / kRowTile + 1 : 0;
+  // of these the block takes key tiles i0 .. i0 + n - 1, of which row tile t sees the first n0, n1
+  const int all = max(all0, all1);
+  const int i0 = all * w.part / w.parts, n = all * (w.part + 1) / w.parts - i0;
+  const int n0 = max(0, min(all0 - i0, n)), n1 = max(0, min(all1 - i0, n));
+  const bool two = rows1 > 0;
 
   if (threadIdx.x == 0) {
     ms.abort_flag = 0;
-    for (int i = 0; i < kRing; ++i) mbar_init(bar(ms.empty[i]), n1 ? 2 : 1);  // the row tiles' MMA warps
+    for (int i = 0; i < kRing; ++i) mbar_init(bar(ms.empty[i]), two ? 2 : 1);  // the row tiles' MMA warps
     for (int t = 0; t < 2; ++t) {
       mbar_init(bar(ms.kfull[t]), 1);
       mbar_init(bar(ms.vfull[t]), 1);
@@ -415,7 +500,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
     int s = 0;
     uint32_t ph = 0;
     for (int i = 0; i < n && ok; ++i) {
-      const int row = (int)(off + (int64_t)i * kRowTile);
+      const int row = (int)(off + (int64_t)(i0 + i) * kRowTile);
       const uint32_t kf = bar(ms.kfull[i & 1]), vf = bar(ms.vfull[i & 1]), par = (uint32_t)(i >> 1) & 1u;
 #pragma unroll 1
       for (int b = 0; b < kKV; ++b) {
@@ -508,31 +593,32 @@ __global__ void __launch_bounds__(kAttThreads, 1)
       }
       return true;
     };
+    bool ok = true;
     if (nt) {
-      bool ok = wait_warp(bar(ms.qfull[t]), 0, ctl) && k_landed(0);
+      ok = wait_warp(bar(ms.qfull[t]), 0, ctl) && k_landed(0);
       if (ok) first(0);
       for (int i = 0; ok && i < nt; ++i) {
         // the tiles take turns, so that one's softmax falls under the other's products (left to themselves they
         // run in step); what a turn needs is waited for before it
         ok = v_landed(i) && wait_warp(bar(ms.pfull[t][0]), (uint32_t)i & 1u, ctl);
-        if (ok && n1 && (t ? i < n0 : i > 0))
+        if (ok && two && (t ? i < n0 : i > 0))
           ok = wait_warp(bar(ms.turn[t]), (uint32_t)(t ? i : i - 1) & 1u, ctl);
         ok = ok && second(i);
         if (ok && i + 1 < nt) {
           ok = k_landed(i + 1);  // (not before the turn: the ring has no room for it much earlier)
           if (ok) first(i + 1);
         }
-        if (ok && n1 && lane == 0) mbar_arrive(bar(ms.turn[t ^ 1]));
+        if (ok && two && lane == 0) mbar_arrive(bar(ms.turn[t ^ 1]));
       }
-      // The blocks of key tiles that only the other row tile needs: handed
-      // back once they have landed, so that no block is handed back twice in
-      // one round of the ring.
-      if (n1)
-        for (int i = nt; ok && i < n; ++i) {
-          ok = k_landed(i) && v_landed(i);
-          if (ok && lane < kKV) mbar_arrive(bar(ms.empty[(kKV * i + lane) % kRing]));
-        }
     }
+    // The blocks of key tiles that only the other row tile sees: handed back
+    // once they have landed, so that no block is handed back twice in one round
+    // of the ring.
+    if (t == 0 || two)
+      for (int i = nt; ok && i < n; ++i) {
+        ok = k_landed(i) && v_landed(i);
+        if (ok && lane < kKV) mbar_arrive(bar(ms.empty[(kKV * i + lane) % kRing]));
+      }
     if (elect()) commit(bar(ms.done[t]));
     __syncwarp();
     drain(bar(ms.done[t]), 0);
@@ -575,8 +661,8 @@ __global__ void __launch_bounds__(kAttThreads, 1)
     }
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t s_at = tmem + lanes + t * 128, o_at = tmem + lanes + kOCol + t * 128;
-    const int pos = pos0 + t * kRowTile + tid;        // this thread's row
-    const int whole = (pos0 + t * kRowTile + 1) / kRowTile;  // key tiles that every row of the tile sees whole
+    const int pos = pos0 + t * kRowTile + tid - i0 * kRowTile;  // this thread's row, from the part's first key
+    const int whole = (pos0 + t * kRowTile + 1) / kRowTile - i0;  // key tiles that every row of the tile sees whole
     const float scale = a.scale_log2;
     float m = -INFINITY, l = 0.f;
     bool ok = true;
@@ -640,7 +726,26 @@ __global__ void __launch_bounds__(kAttThreads, 1)
       l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
     }
     if (ok && nt) ok = wait_warp(bar(ms.ofull[t]), 0, ctl);
-    if (ok && nt) {
+    if (ok && w.parts > 1) {
+      // a part: unnormalised, for the join
+      const int64_t at = (int64_t)w.slot * 2 * kRowTile + t * kRowTile + tid;
+      if (tid < rows) a.part_ml[at] = make_float2(m, l);
+      if (nt) {
+        fence_after();
+#pragma unroll 1
+        for (int c = 0; c < 8; ++c) {
+          uint32_t o[16];
+          tmem_ld16(o_at + c * 16, o);
+          tmem_wait_ld();
+          if (tid < rows) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              *reinterpret_cast<uint4*>(a.part + at * kDV + c * 16 + 4 * k) =
+                  make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+          }
+        }
+      }
+    } else if (ok && nt) {
       fence_after();
       const float norm = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
       __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(a.out) + ((token0 + tid) * a.H + h) * kDV;
@@ -667,6 +772,58 @@ __global__ void __launch_bounds__(kAttThreads, 1)
   __syncthreads();
   fence_after();
   if (warp == 9) tmem_dealloc(tmem, 512);
+}
+
+// Joins the parts of the tail's units: a warp a row, in part order.  grid
+// (units, 32 groups of 8 rows).
+__global__ void __launch_bounds__(256) k_prefill_join(const __grid_constant__ PrefillArgs a) {
+  __shared__ Plan p;
+  make_plan(a, p);  // (the lengths were there before the attention started)
+  pdl_enter();
+  const int tail = tail_of(a, p), x = blockIdx.x;
+  if (x >= tail) return;
+  const int u = p.used * a.H - tail + x;
+  const Unit w = unit_at(a, p, u);
+  const int most = min(kTail / tail, kMaxParts);
+  const int parts = parts_of(tail, p.tiles[p.order[a.Q == 1 ? u % p.used : u / a.H]]);
+  if (parts == 1) return;
+  const Chunk ch = prefill_chunk(a, w.q, false);
+  const int row = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  {
+    const LatentCache& C = a.cache;
+    int bad = 0;
+    for (int i = threadIdx.x; i <= (ch.end - 1) >> C.log2b; i += 256) {
+      const int page = C.bt[(int64_t)w.q * C.bt_stride + i];
+      bad |= page < 0 || page >= C.num_pages;
+    }
+    if (__syncthreads_or(bad)) return;
+  }
+  if (w.r0 + row >= ch.count) return;
+  const int64_t at0 = (int64_t)x * most * 2 * kRowTile + row;
+  const float2 ml = lane < parts ? a.part_ml[at0 + (int64_t)lane * 2 * kRowTile] : make_float2(-INFINITY, 0.f);
+  float m = ml.x;
+#pragma unroll
+  for (int d = 16; d >= 1; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+  const float wt = m == -INFINITY ? 0.f : exp2f(ml.x - m);
+  float l = ml.y * wt;
+#pragma unroll
+  for (int d = 16; d >= 1; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i = 0; i < parts; ++i) {
+    const float wi = __shfl_sync(0xffffffffu, wt, i);
+    if (wi == 0.f) continue;
+    const float4 v = *reinterpret_cast<const float4*>(a.part + (at0 + (int64_t)i * 2 * kRowTile) * kDV + 4 * lane);
+    o.x = fmaf(wi, v.x, o.x);
+    o.y = fmaf(wi, v.y, o.y);
+    o.z = fmaf(wi, v.z, o.z);
+    o.w = fmaf(wi, v.w, o.w);
+  }
+  const float norm = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+  uint2 v;
+  v.x = pack_bf16(o.x * norm, o.y * norm);
+  v.y = pack_bf16(o.z * norm, o.w * norm);
+  *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(a.out) +
+                            (((int64_t)w.q * a.rows + w.r0 + row) * a.H + w.h) * kDV + 4 * lane) = v;
 }
 
 }  // namespace
@@ -701,9 +858,16 @@ cudaError_t launch_prefill_tc(const PrefillArgs& a, void* encode_fn, int sms, cu
     e = cudaLaunchKernelEx(&l.cfg, k_expand_tc, a, mc, mw, mkv);
   }
   if (e != cudaSuccess) return e;
-  PdlLaunch l(dim3((unsigned)((a.rows + 2 * kRowTile - 1) / (2 * kRowTile)), (unsigned)a.H, (unsigned)a.Q),
-              dim3(kAttThreads), kAttSmem, s);
-  return cudaLaunchKernelEx(&l.cfg, k_prefill_tc, a, mkv, mkr);
+  const int64_t classes = (int64_t)a.Q * ((a.rows + 2 * kRowTile - 1) / (2 * kRowTile));
+  PrefillArgs b = a;
+  b.planned = classes <= kPlanClasses;
+  {
+    PdlLaunch l(dim3((unsigned)(classes * a.H + (b.planned ? kTail : 0))), dim3(kAttThreads), kAttSmem, s);
+    e = cudaLaunchKernelEx(&l.cfg, k_prefill_tc, b, mkv, mkr);
+  }
+  if (e != cudaSuccess || !b.planned) return e;
+  PdlLaunch l(dim3((unsigned)std::min<int64_t>(kTail - 1, classes * a.H), 32), dim3(256), 0, s);
+  return cudaLaunchKernelEx(&l.cfg, k_prefill_join, b);
 }
 
 }  // namespace spin

@@ -103,10 +103,12 @@ Carve carve(const spin_latent_config* c) {
   // hold fewer heads than its slots.
   const int group = std::min(kTcHeads, (c->num_heads + 15) / 16 * 16);
   const size_t heads = std::max<size_t>((size_t)2 * kTcBlocks * group, (size_t)2 * kSimtBlocks * kSimtHeads);
+  // (the expanded form's parts take the same place: 256 rows of each of 148 blocks)
+  const size_t parts = c->prefill_slots ? (size_t)kTcBlocks * 256 : 0;
   k.err = take(sizeof(ErrWord));
   k.turn = take(kMaxRopeDim / 2 * sizeof(uint64_t));
-  k.ml = take(heads * sizeof(float2));
-  k.part = take(heads * c->latent_dim * sizeof(float));
+  k.ml = take(std::max(heads, parts) * sizeof(float2));
+  k.part = take(std::max(heads * c->latent_dim, parts * c->v_dim) * sizeof(float));
   k.kv = take(c->prefill_slots ? (size_t)c->prefill_slots * c->num_heads * (c->nope_dim + c->v_dim) * el : 0);
   k.kr = take(c->prefill_slots ? (size_t)c->prefill_slots * c->rope_dim * el : 0);
   k.total = off;
@@ -371,6 +373,8 @@ spin_status spin_latent_prefill(spin_latent lt, int rows, const void* cache, int
   a.out = out;
   a.kv = lt->kv;
   a.kr = lt->kr;
+  a.part = lt->part;
+  a.part_ml = lt->part_ml;
   a.scale_log2 = (float)((double)c.softmax_scale * 1.4426950408889634);
   a.err = lt->err;
   const int bf16 = c.dtype == SPIN_BF16;

@@ -28,7 +28,8 @@ def _cfg(**over):
 def _expected_bytes(H, dc, dr, dn, dv, cap, el):
     a = lambda x: (x + 255) // 256 * 256
     heads = max(2 * 148 * min(64, -(-H // 16) * 16), 2 * 296 * 8)  # shares: two per block, of the larger kernel
-    return a(16) + a(64 * 8) + a(heads * 8) + a(heads * dc * 4) + a(cap * H * (dn + dv) * el) + a(cap * dr * el)
+    parts = 148 * 256 if cap else 0  # rows of the expanded form's parts, in the same place
+    return a(16) + a(64 * 8) + a(max(heads, parts) * 8) + a(max(heads * dc, parts * dv) * 4) + a(cap * H * (dn + dv) * el) + a(cap * dr * el)
 
 
 @pytest.mark.parametrize("over", [{}, {"num_heads": 128}, {"num_heads": 1}, {"bf16": False}, {"prefill_slots": 0},
