@@ -2,9 +2,10 @@
 // cores: bf16, latent width 512, key width 128 + 64 (rotary), value width 128.
 //
 // k_expand_tc   [k | v] = W_h c for every slot and head, into the workspace: a
-//               matrix product M = slots, N = 256, K = 512.  A block keeps the
-//               latents of 128 slots (128 KB) and streams the heads' weights, so
-//               L2 -> SM carries 256 KB a 4096-cycle tile instead of 384.
+//               matrix product M = slots, N = 128 twice, K = 512.  A block keeps
+//               the latents of 128 slots in TMEM and streams the heads' weights,
+//               160 KB in flight, so L2 -> SM carries 256 KB a 4096-cycle unit
+//               instead of 384.
 // k_prefill_tc  causal attention of 256 rows of one head: two 128-row tiles take
 //               turns on the tensor cores, one's softmax under the other's
 //               products:
@@ -34,14 +35,16 @@ constexpr float kLazy = 8.0f;
 // ---------------------------------------------------------------------------
 // expansion
 // ---------------------------------------------------------------------------
-constexpr int kExpThreads = 192;     // warps 0..3 epilogue, 4 copies, 5 MMA issue
-constexpr int kABlocks = kDC / 64;   // 8
-constexpr int kBBytes = kN * 128;    // 256 weights' rows of 64 columns
-constexpr int kBStages = 2;
-constexpr int kOutBufs = 2;          // 16 KB blocks on their way out
+constexpr int kExpThreads = 320;     // warps 0..3 the keys' epilogue, 4..7 latents and the values', 8 copies, 9 MMA issue
+constexpr int kHalf = kN / 2;        // a unit's product is taken in two halves, the keys and the values
+constexpr int kStageK = 128;         // reduction width of a stage of weights
+constexpr int kBBytes = kHalf * kStageK * 2;
+constexpr int kBStages = 5;
+constexpr int kOutBufs = 2;          // 16 KB blocks of each half on their way out
+constexpr uint32_t kACol = 256;      // the latents in TMEM, behind the two accumulators
 
 struct ExpMisc {
-  uint64_t afull[kABlocks], afree;   // latents of a slot tile
+  uint64_t afull;                    // latents of a slot tile
   uint64_t bfull[kBStages], bfree[kBStages];
   uint64_t dfull[2], dfree[2];       // accumulators
   uint64_t done;
@@ -49,7 +52,7 @@ struct ExpMisc {
   uint32_t tmem;
   int abort_flag;
 };
-constexpr uint32_t kExpSmem = 1024 + kABlocks * kBlk + kBStages * kBBytes + kOutBufs * kBlk + sizeof(ExpMisc);
+constexpr uint32_t kExpSmem = 1024 + kBStages * kBBytes + 2 * kOutBufs * kBlk + sizeof(ExpMisc);
 static_assert(kExpSmem <= 227 * 1024, "one block's shared memory");
 
 // The walk over units (slot tile, head), heads within a tile.
@@ -76,22 +79,20 @@ struct ExpWalk {
 };
 
 __global__ void __launch_bounds__(kExpThreads, 1)
-    k_expand_tc(const __grid_constant__ PrefillArgs a, const __grid_constant__ CUtensorMap map_c,
-                const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_kv) {
+    k_expand_tc(const __grid_constant__ PrefillArgs a, const __grid_constant__ CUtensorMap map_w,
+                const __grid_constant__ CUtensorMap map_kv) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* a_sm = smem;
-  uint8_t* b_sm = a_sm + kABlocks * kBlk;
+  uint8_t* b_sm = smem;
   uint8_t* o_sm = b_sm + kBStages * kBBytes;
-  ExpMisc& ms = *reinterpret_cast<ExpMisc*>(o_sm + kOutBufs * kBlk);
-  const uint32_t a_at = smem_u32(a_sm), b_at = smem_u32(b_sm), o_at = smem_u32(o_sm);
+  ExpMisc& ms = *reinterpret_cast<ExpMisc*>(o_sm + 2 * kOutBufs * kBlk);
+  const uint32_t b_at = smem_u32(b_sm), o_at = smem_u32(o_sm);
   auto bar = [](uint64_t& b) { return smem_u32(&b); };
   const Ctl ctl{&ms.abort_flag, a.err};
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     ms.abort_flag = 0;
-    for (int i = 0; i < kABlocks; ++i) mbar_init(bar(ms.afull[i]), 1);
-    mbar_init(bar(ms.afree), 1);
+    mbar_init(bar(ms.afull), 4);
     for (int i = 0; i < kBStages; ++i) {
       mbar_init(bar(ms.bfull[i]), 1);
       mbar_init(bar(ms.bfree[i]), 1);
@@ -103,7 +104,7 @@ __global__ void __launch_bounds__(kExpThreads, 1)
     mbar_init(bar(ms.done), 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 5) tmem_alloc(smem_u32(&ms.tmem), 512);
+  if (warp == 9) tmem_alloc(smem_u32(&ms.tmem), 512);
   fence_before();
   __syncthreads();
   fence_after();
@@ -160,47 +161,24 @@ __global__ void __launch_bounds__(kExpThreads, 1)
 
   if (!n_units) {
     // more blocks than units
-  } else if (warp == 4) {
-    // ======================= copies =======================
-    const LatentCache& C = a.cache;
-    const int box = min(C.b, kSlotTile), boxes = kSlotTile / box;  // rows of a copy, copies a block
-    const int none = C.num_pages << C.log2b;                       // a row outside the cache: zeros
-    int st = 0, seen = -1, q_seen = -1, nload = 0;
+  } else if (warp == 8) {
+    // ======================= copies of the weights =======================
+    int st = 0;
     uint32_t ph = 0;
     bool ok = true;
-    uint32_t a_armed = 0, b_armed[kBStages] = {2, 2};
+    uint32_t armed[kBStages];
+    for (int i = 0; i < kBStages; ++i) armed[i] = 2;
     for (int i = 0; i < n_units && ok; ++i) {
-      if (w.tile != seen || w.q != q_seen) {
-        seen = w.tile;
-        q_seen = w.q;
-        int row = none;
-        const int slot = w.tile * kSlotTile + lane * box;
-        if (lane < boxes && slot < w.end) {
-          const int page = C.bt[(int64_t)w.q * C.bt_stride + (slot >> C.log2b)];
-          if (page >= 0 && page < C.num_pages)
-            row = (page << C.log2b) + (slot & (C.b - 1));
-          else
-            raise_error(a.err, ERR_PAGE, w.q, (uint32_t)page);
-        }
-        ok = wait_warp(bar(ms.afree), (uint32_t)nload & 1u ^ 1u, ctl);
-        if (!ok) break;
-        if (lane == 0)
-          for (int k = 0; k < kABlocks; ++k) mbar_expect_tx(bar(ms.afull[k]), kBlk);
-        ++nload;
-        a_armed = 1;
-        __syncwarp();
-        if (lane < boxes)
-          for (int k = 0; k < kABlocks; ++k)
-            tma_load_2d(a_at + k * kBlk + lane * box * 128, &map_c, bar(ms.afull[k]), k * 64, row);
-      }
-      for (int k = 0; k < kABlocks; ++k) {
+      for (int x = 0; x < 2 * kDC / kStageK; ++x) {
+        const int k = x % (kDC / kStageK) * kStageK, row = w.h * kN + x / (kDC / kStageK) * kHalf;
         ok = wait_warp(bar(ms.bfree[st]), ph ^ 1u, ctl);
         if (!ok) break;
         if (lane == 0) {
           mbar_expect_tx(bar(ms.bfull[st]), kBBytes);
-          tma_load_2d(b_at + st * kBBytes, &map_w, bar(ms.bfull[st]), k * 64, w.h * kN);
+          for (int c = 0; c < kStageK / 64; ++c)
+            tma_load_2d(b_at + st * kBBytes + c * kBlk, &map_w, bar(ms.bfull[st]), k + c * 64, row);
         }
-        b_armed[st] = ph;
+        armed[st] = ph;
         if (++st == kBStages) {
           st = 0;
           ph ^= 1u;
@@ -208,113 +186,140 @@ __global__ void __launch_bounds__(kExpThreads, 1)
       }
       w.step(a);
     }
-    if (lane == 0 && ms.abort_flag) {
-      if (a_armed)
-        for (int k = 0; k < kABlocks; ++k) drain(bar(ms.afull[k]), (uint32_t)(nload - 1) & 1u);
+    if (lane == 0 && ms.abort_flag)
       for (int s = 0; s < kBStages; ++s)
-        if (b_armed[s] < 2) drain(bar(ms.bfull[s]), b_armed[s]);
-    }
-  } else if (warp == 5) {
+        if (armed[s] < 2) drain(bar(ms.bfull[s]), armed[s]);
+  } else if (warp == 9) {
     // ======================= MMA issue =======================
-    const uint32_t id = idesc_bf16(128, kN, 0, 0);
+    const uint32_t id = idesc_bf16(128, kHalf, 0, 0);
     int st = 0, nload = -1, seen = -1, q_seen = -1;
     uint32_t ph = 0;
     bool ok = true;
     for (int i = 0; i < n_units && ok; ++i) {
-      const bool fresh = w.tile != seen || w.q != q_seen;
-      if (fresh) {
+      if (w.tile != seen || w.q != q_seen) {
         seen = w.tile;
         q_seen = w.q;
         ++nload;
+        ok = wait_warp(bar(ms.afull), (uint32_t)nload & 1u, ctl);
       }
-      const uint32_t d = tmem + (uint32_t)(i & 1) * kN;
-      ok = wait_warp(bar(ms.dfree[i & 1]), (uint32_t)(i >> 1) & 1u ^ 1u, ctl);
-      for (int k = 0; k < kABlocks && ok; ++k) {
-        if (fresh) ok = wait_warp(bar(ms.afull[k]), (uint32_t)nload & 1u, ctl);
-        ok = ok && wait_warp(bar(ms.bfull[st]), ph, ctl);
-        if (!ok) break;
-        fence_after();
-        const uint64_t ad = sw128_desc(a_at + k * kBlk, 16, 1024), bd = sw128_desc(b_at + st * kBBytes, 16, 1024);
-        if (elect()) {
+      for (int half = 0; half < 2 && ok; ++half) {
+        const uint32_t d = tmem + (uint32_t)half * kHalf;
+        ok = wait_warp(bar(ms.dfree[half]), (uint32_t)i & 1u ^ 1u, ctl);
+        for (int x = 0; x < kDC / kStageK && ok; ++x) {
+          ok = wait_warp(bar(ms.bfull[st]), ph, ctl);
+          if (!ok) break;
+          fence_after();
+          const uint64_t bd = sw128_desc(b_at + st * kBBytes, 16, 1024);
+          const uint32_t at = tmem + kACol + (uint32_t)x * (kStageK / 2);
+          const uint32_t joined = x > 0;
+          if (elect()) {
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk) mma_f16(d, ad + 2 * kk, bd + 2 * kk, id, k > 0 || kk > 0 ? 1u : 0u);
-          commit(bar(ms.bfree[st]));
-        }
-        __syncwarp();
-        if (++st == kBStages) {
-          st = 0;
-          ph ^= 1u;
+            for (int kk = 0; kk < kStageK / 16; ++kk)
+              mma_f16_ts(d, at + kk * 8, bd + (kk >> 2) * (kBlk >> 4) + 2 * (kk & 3), id, kk > 0 ? 1u : joined);
+            commit(bar(ms.bfree[st]));
+            if (x == kDC / kStageK - 1) commit(bar(ms.dfull[half]));
+          }
+          __syncwarp();
+          if (++st == kBStages) {
+            st = 0;
+            ph ^= 1u;
+          }
         }
       }
-      if (!ok) break;
       w.step(a);
-      const bool leave = i + 1 < n_units && (w.tile != seen || w.q != q_seen);
-      if (elect()) {
-        commit(bar(ms.dfull[i & 1]));
-        if (leave) commit(bar(ms.afree));
-      }
-      __syncwarp();
     }
     if (elect()) commit(bar(ms.done));
     __syncwarp();
     drain(bar(ms.done), 0);
   } else {
-    // ======================= epilogue =======================
-    const int row = warp * 32 + lane;
-    const uint32_t lanes = (uint32_t)(warp * 32) << 16;
+    // ======================= latents and epilogue =======================
+    const int half = warp >> 2, row = (warp & 3) * 32 + lane;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const LatentCache& C = a.cache;
+    // A slot tile's latents: a thread's slot into its TMEM lane, two elements a
+    // column.  Slots past the request's last become zeros, and so do their keys
+    // and values: a weight of 0 must meet no NaN.  The rotary part goes
+    // straight to the workspace.
+    auto load = [&](const ExpWalk& w) {
+      const int slot = w.tile * kSlotTile + row;
+      const uint4* src = nullptr;
+      if (slot < w.end) {
+        const int page = C.bt[(int64_t)w.q * C.bt_stride + (slot >> C.log2b)];
+        if (page >= 0 && page < C.num_pages)
+          src = reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(C.data) +
+                                               (((int64_t)page << C.log2b) + (slot & (C.b - 1))) * (kDC + kDR));
+        else
+          raise_error(a.err, ERR_PAGE, w.q, (uint32_t)page);
+      }
+#pragma unroll 1
+      for (int c = 0; c < kDC / 64; ++c) {
+        uint32_t v[32];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const uint4 x = src ? src[8 * c + k] : make_uint4(0, 0, 0, 0);
+          v[4 * k] = x.x;
+          v[4 * k + 1] = x.y;
+          v[4 * k + 2] = x.z;
+          v[4 * k + 3] = x.w;
+        }
+        tmem_st32(tmem + lanes + kACol + (uint32_t)c * 32, v);
+      }
+      tmem_wait_st();
+      fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(ms.afull));
+      if (w.h == 0) {  // (a tile that another block begins has its rotary part from there)
+        uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(a.kr) + (w.off + slot) * kDR);
+#pragma unroll
+        for (int c = 0; c < kDR / 8; ++c) dst[c] = src ? src[kDC / 8 + c] : make_uint4(0, 0, 0, 0);
+      }
+    };
+    const bool store = (threadIdx.x & 127) == 0;  // the half's thread that issues its stores
+    if (half) load(w);
     int buf = 0;
     for (int i = 0; i < n_units; ++i) {
-      const int slot = w.tile * kSlotTile + row;
-      const bool live = slot < w.end;  // rows past the request's slots become zeros: a weight of 0 must meet no NaN
-      if (w.h == 0) {
-        uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(a.kr) + (w.off + slot) * kDR);
-        const uint4* src = nullptr;
-        if (live) {
-          const int page = C.bt[(int64_t)w.q * C.bt_stride + (slot >> C.log2b)];
-          if (page >= 0 && page < C.num_pages)
-            src = reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(C.data) +
-                                                 (((int64_t)page << C.log2b) + (slot & (C.b - 1))) * (kDC + kDR) + kDC);
-        }
-#pragma unroll
-        for (int c = 0; c < kDR / 8; ++c) dst[c] = src ? src[c] : make_uint4(0, 0, 0, 0);
-      }
-      const bool ok = wait_warp(bar(ms.dfull[i & 1]), (uint32_t)(i >> 1) & 1u, ctl);
-      if (bar_or(1, 128, !ok)) break;  // (the warps leave together: they meet at barriers below)
+      const bool ok = wait_warp(bar(ms.dfull[half]), (uint32_t)i & 1u, ctl);
+      if (bar_or(1 + half, 128, !ok)) break;  // (the warps leave together: they meet at barriers below)
       fence_after();
+      if (half && i + 1 < n_units) {
+        // every product of this tile is complete: the next tile's latents first, so that its products begin
+        ExpWalk next = w;
+        next.step(a);
+        if (next.tile != w.tile || next.q != w.q) load(next);
+      }
 #pragma unroll 1
-      for (int c = 0; c < kN / 64; ++c) {
+      for (int c = 0; c < kHalf / 64; ++c) {
         uint32_t v[2][32];
-        tmem_ld32(tmem + lanes + (uint32_t)((i & 1) * kN + c * 64), v[0]);
-        tmem_ld32(tmem + lanes + (uint32_t)((i & 1) * kN + c * 64 + 32), v[1]);
+        tmem_ld32(tmem + lanes + (uint32_t)(half * kHalf + c * 64), v[0]);
+        tmem_ld32(tmem + lanes + (uint32_t)(half * kHalf + c * 64 + 32), v[1]);
         tmem_wait_ld();
+        if (c == kHalf / 64 - 1) {  // the accumulator is in registers: hand it back
+          fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(ms.dfree[half]));
+        }
         // the block's buffer: its store two blocks ago has read it
-        if (threadIdx.x == 0) asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kOutBufs - 1) : "memory");
-        bar_sync(1, 128);
-        const uint32_t dst = o_at + buf * kBlk + row * 128;
+        if (store) asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kOutBufs - 1) : "memory");
+        bar_sync(1 + half, 128);
+        const uint32_t out = o_at + (half * kOutBufs + buf) * kBlk, dst = out + row * 128;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           uint32_t p[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const int x = 8 * j + 2 * e;
-            p[e] = live ? pack_bf16(__uint_as_float(v[x >> 5][x & 31]), __uint_as_float(v[x >> 5][(x & 31) + 1])) : 0u;
+            p[e] = pack_bf16(__uint_as_float(v[x >> 5][x & 31]), __uint_as_float(v[x >> 5][(x & 31) + 1]));
           }
           asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + ((j ^ (row & 7)) << 4)), "r"(p[0]),
                        "r"(p[1]), "r"(p[2]), "r"(p[3])
                        : "memory");
         }
-        if (c == kN / 64 - 1) {  // the accumulator is in registers: hand it back
-          fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar(ms.dfree[i & 1]));
-        }
         fence_async_smem();
-        bar_sync(1, 128);
-        if (threadIdx.x == 0) {
+        bar_sync(1 + half, 128);
+        if (store) {
           asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
                            (uint64_t)&map_kv),
-                       "r"(o_at + buf * kBlk), "r"(c * 64), "r"((int)(w.h * a.cap + w.off + w.tile * kSlotTile))
+                       "r"(out), "r"(half * kHalf + c * 64), "r"((int)(w.h * a.cap + w.off + w.tile * kSlotTile))
                        : "memory");
           asm volatile("cp.async.bulk.commit_group;" ::: "memory");
         }
@@ -322,13 +327,13 @@ __global__ void __launch_bounds__(kExpThreads, 1)
       }
       w.step(a);
     }
-    if (threadIdx.x == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    if (store) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   }
 
   fence_before();
   __syncthreads();
   fence_after();
-  if (warp == 5) tmem_dealloc(tmem, 512);
+  if (warp == 9) tmem_dealloc(tmem, 512);
 }
 
 // ---------------------------------------------------------------------------
@@ -774,8 +779,9 @@ __global__ void __launch_bounds__(kAttThreads, 1)
   if (warp == 9) tmem_dealloc(tmem, 512);
 }
 
-// Joins the parts of the tail's units: a warp a row, in part order.  grid
-// (units, 32 groups of 8 rows).
+// Joins the parts of the tail's units: a warp a row at a time, in part order.
+// grid (units, kJoinGroups groups of rows); few blocks, since each makes the plan.
+constexpr int kJoinGroups = 4;
 __global__ void __launch_bounds__(256) k_prefill_join(const __grid_constant__ PrefillArgs a) {
   __shared__ Plan p;
   make_plan(a, p);  // (the lengths were there before the attention started)
@@ -788,7 +794,7 @@ __global__ void __launch_bounds__(256) k_prefill_join(const __grid_constant__ Pr
   const int parts = parts_of(tail, p.tiles[p.order[a.Q == 1 ? u % p.used : u / a.H]]);
   if (parts == 1) return;
   const Chunk ch = prefill_chunk(a, w.q, false);
-  const int row = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31;
   {
     const LatentCache& C = a.cache;
     int bad = 0;
@@ -798,41 +804,45 @@ __global__ void __launch_bounds__(256) k_prefill_join(const __grid_constant__ Pr
     }
     if (__syncthreads_or(bad)) return;
   }
-  if (w.r0 + row >= ch.count) return;
-  const int64_t at0 = (int64_t)x * most * 2 * kRowTile + row;
-  const float2 ml = lane < parts ? a.part_ml[at0 + (int64_t)lane * 2 * kRowTile] : make_float2(-INFINITY, 0.f);
-  float m = ml.x;
+  const int64_t at0 = (int64_t)x * most * 2 * kRowTile;
+  const int rows = min(2 * kRowTile, ch.count - w.r0);
+  for (int row = blockIdx.y * 8 + (threadIdx.x >> 5); row < rows; row += kJoinGroups * 8) {
+    const float2 ml = lane < parts ? a.part_ml[at0 + (int64_t)lane * 2 * kRowTile + row] : make_float2(-INFINITY, 0.f);
+    float m = ml.x;
 #pragma unroll
-  for (int d = 16; d >= 1; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-  const float wt = m == -INFINITY ? 0.f : exp2f(ml.x - m);
-  float l = ml.y * wt;
+    for (int d = 16; d >= 1; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+    const float wt = m == -INFINITY ? 0.f : exp2f(ml.x - m);
+    float l = ml.y * wt;
 #pragma unroll
-  for (int d = 16; d >= 1; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int i = 0; i < parts; ++i) {
-    const float wi = __shfl_sync(0xffffffffu, wt, i);
-    if (wi == 0.f) continue;
-    const float4 v = *reinterpret_cast<const float4*>(a.part + (at0 + (int64_t)i * 2 * kRowTile) * kDV + 4 * lane);
-    o.x = fmaf(wi, v.x, o.x);
-    o.y = fmaf(wi, v.y, o.y);
-    o.z = fmaf(wi, v.z, o.z);
-    o.w = fmaf(wi, v.w, o.w);
+    for (int d = 16; d >= 1; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int i = 0; i < parts; ++i) {
+      const float wi = __shfl_sync(0xffffffffu, wt, i);
+      const float4 v = wi != 0.f ? *reinterpret_cast<const float4*>(
+                                       a.part + (at0 + (int64_t)i * 2 * kRowTile + row) * kDV + 4 * lane)
+                                 : make_float4(0.f, 0.f, 0.f, 0.f);
+      o.x = fmaf(wi, v.x, o.x);
+      o.y = fmaf(wi, v.y, o.y);
+      o.z = fmaf(wi, v.z, o.z);
+      o.w = fmaf(wi, v.w, o.w);
+    }
+    const float norm = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+    uint2 v;
+    v.x = pack_bf16(o.x * norm, o.y * norm);
+    v.y = pack_bf16(o.z * norm, o.w * norm);
+    *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(a.out) +
+                              (((int64_t)w.q * a.rows + w.r0 + row) * a.H + w.h) * kDV + 4 * lane) = v;
   }
-  const float norm = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
-  uint2 v;
-  v.x = pack_bf16(o.x * norm, o.y * norm);
-  v.y = pack_bf16(o.z * norm, o.w * norm);
-  *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(a.out) +
-                            (((int64_t)w.q * a.rows + w.r0 + row) * a.H + w.h) * kDV + 4 * lane) = v;
 }
 
 }  // namespace
 
 bool prefill_tc_supported(const PrefillArgs& a, int bf16) {
-  // rows are the tensor maps' 32-bit coordinates; units fit 31 bits
+  // workspace rows are the tensor maps' 32-bit coordinates; units fit 31 bits
   return bf16 && a.cache.dc == kDC && a.cache.dr == kDR && a.dn == kDN && a.dv == kDV &&
          ((uintptr_t)a.cache.data & 15) == 0 && ((uintptr_t)a.w & 15) == 0 && ((uintptr_t)a.out & 15) == 0 &&
-         ((int64_t)a.cache.num_pages << a.cache.log2b) < (int64_t(1) << 31) - kSlotTile &&
+         ((int64_t)a.cache.num_pages << a.cache.log2b) < (int64_t(1) << 31) &&
          a.cap * a.H < (int64_t(1) << 31);
 }
 
@@ -844,18 +854,15 @@ cudaError_t prepare_prefill_tc() {
 }
 
 cudaError_t launch_prefill_tc(const PrefillArgs& a, void* encode_fn, int sms, cudaStream_t s) {
-  CUtensorMap mc, mw, mkv, mkr;
-  const uint64_t rows = (uint64_t)a.cache.num_pages << a.cache.log2b;
-  const uint32_t box = (uint32_t)(a.cache.b < kSlotTile ? a.cache.b : kSlotTile);
-  if (!encode_rows(encode_fn, &mc, a.cache.data, rows, kDC + kDR, (kDC + kDR) * 2, box) ||
-      !encode_rows(encode_fn, &mw, a.w, (uint64_t)a.H * kN, kDC, kDC * 2, kN) ||
+  CUtensorMap mw, mkv, mkr;
+  if (!encode_rows(encode_fn, &mw, a.w, (uint64_t)a.H * kN, kDC, kDC * 2, kHalf) ||
       !encode_rows(encode_fn, &mkv, a.kv, (uint64_t)a.H * a.cap, kN, kN * 2, kRowTile) ||
       !encode_rows(encode_fn, &mkr, a.kr, (uint64_t)a.cap, kDR, kDR * 2, kRowTile))
     return cudaErrorInvalidValue;
   cudaError_t e;
   {
     PdlLaunch l(dim3((unsigned)sms), dim3(kExpThreads), kExpSmem, s);
-    e = cudaLaunchKernelEx(&l.cfg, k_expand_tc, a, mc, mw, mkv);
+    e = cudaLaunchKernelEx(&l.cfg, k_expand_tc, a, mw, mkv);
   }
   if (e != cudaSuccess) return e;
   const int64_t classes = (int64_t)a.Q * ((a.rows + 2 * kRowTile - 1) / (2 * kRowTile));
@@ -866,7 +873,7 @@ cudaError_t launch_prefill_tc(const PrefillArgs& a, void* encode_fn, int sms, cu
     e = cudaLaunchKernelEx(&l.cfg, k_prefill_tc, b, mkv, mkr);
   }
   if (e != cudaSuccess || !b.planned) return e;
-  PdlLaunch l(dim3((unsigned)std::min<int64_t>(kTail - 1, classes * a.H), 32), dim3(256), 0, s);
+  PdlLaunch l(dim3((unsigned)std::min<int64_t>(kTail - 1, classes * a.H), kJoinGroups), dim3(256), 0, s);
   return cudaLaunchKernelEx(&l.cfg, k_prefill_join, b);
 }
 
