@@ -544,76 +544,80 @@ __global__ void __launch_bounds__(kAttThreads, 1)
     const uint32_t id_o = idesc_bf16(128, 128, 0, 1), id_o64 = idesc_bf16(128, 64, 0, 1);
     const uint32_t s_col = tmem + t * 128, o_col = tmem + kOCol + t * 128;
     // ring blocks of K(i): 5 i .. + 2, of V(i): 5 i + 3, 5 i + 4
-    auto k_landed = [&](int i) { return wait_warp(bar(ms.kfull[i & 1]), (uint32_t)(i >> 1) & 1u, ctl); };
-    auto v_landed = [&](int i) { return wait_warp(bar(ms.vfull[i & 1]), (uint32_t)(i >> 1) & 1u, ctl); };
-    auto first = [&](int i) {  // S(i)
-      const int x = kKV * i;
-      uint64_t bd[kKBlocks];
+    const uint64_t ad = sw128_desc(q_at + t * kKBlocks * kBlk, 16, 1024);
+    // The elected lane's parts of a turn, in loops of four instructions: the
+    // warp shares its instruction cache with the softmax, and a turn written out
+    // took longer to fetch than to run.  S(i), 64 columns b of K at ring block s:
+    auto first = [&](int b, int s) {
+      const uint64_t aq = ad + (uint64_t)b * (kBlk >> 4), bd = sw128_desc(r_at + s * kBlk, 16, 1024);
+      const uint32_t joined = b > 0;
 #pragma unroll
-      for (int b = 0; b < kKBlocks; ++b) bd[b] = sw128_desc(r_at + (x + b) % kRing * kBlk, 16, 1024);
-      const uint64_t ad = sw128_desc(q_at + t * kKBlocks * kBlk, 16, 1024);
-      fence_after();
-      if (elect()) {
-#pragma unroll
-        for (int b = 0; b < kKBlocks; ++b) {
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            mma_f16(s_col, ad + b * (kBlk >> 4) + 2 * kk, bd[b] + 2 * kk, id_s, b > 0 || kk > 0 ? 1u : 0u);
-          commit(bar(ms.empty[(x + b) % kRing]));
-        }
-        commit(bar(ms.sfull[t]));
-      }
-      __syncwarp();
+      for (int kk = 0; kk < 4; ++kk) mma_f16(s_col, aq + 2 * kk, bd + 2 * kk, id_s, kk > 0 ? 1u : joined);
+      commit(bar(ms.empty[s]));
     };
-    auto second = [&](int i) -> bool {  // O += P(i) V(i)
-      const int x = kKV * i + kKBlocks, s = x % kRing;
-      const uint64_t bd = sw128_desc(r_at + s * kBlk, kBlk, 1024), be = sw128_desc(r_at, kBlk, 1024);
-      const uint32_t joined = i > 0;
-      // V's two blocks as one operand 128 wide (with N = 64 an instruction takes as long), but where the ring ends
-      // between them
-      const bool split = s == kRing - 1;
+    // O += P(i) V(i), 64 keys, V at ring blocks s, s + 1.  V's two blocks are one operand 128 wide (with N = 64 an
+    // instruction takes as long), but where the ring ends between them.
+    auto second = [&](int half, int s, uint32_t joined) {
+      const uint64_t step = (uint64_t)half * (4 * 2048 >> 4);
+      const uint64_t bd = sw128_desc(r_at + s * kBlk, kBlk, 1024) + step, be = sw128_desc(r_at, kBlk, 1024) + step;
+      const uint32_t p = s_col + half * 32;
+      if (s != kRing - 1) {
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        if (half && !wait_warp(bar(ms.pfull[t][1]), (uint32_t)i & 1u, ctl)) return false;
-        fence_after();
-        if (elect()) {
-#pragma unroll
-          for (int kk = 4 * half; kk < 4 * half + 4; ++kk) {
-            const uint32_t acc = kk > 0 ? 1u : joined;
-            const uint64_t step = (uint64_t)kk * (2048 >> 4);
-            if (!split) {
-              mma_f16_ts(o_col, s_col + kk * 8, bd + step, id_o, acc);
-            } else {
-              mma_f16_ts(o_col, s_col + kk * 8, bd + step, id_o64, acc);
-              mma_f16_ts(o_col + 64, s_col + kk * 8, be + step, id_o64, acc);
-            }
-          }
-          if (half == 1) {
-            commit(bar(ms.empty[s]));
-            commit(bar(ms.empty[(x + 1) % kRing]));
-            if (i + 1 == nt) commit(bar(ms.ofull[t]));
-          }
+        for (int k = 0; k < 4; ++k) mma_f16_ts(o_col, p + k * 8, bd + k * (2048 >> 4), id_o, k > 0 ? 1u : joined);
+      } else {
+#pragma unroll 1
+        for (int k = 0; k < 4; ++k) {
+          mma_f16_ts(o_col, p + k * 8, bd + k * (2048 >> 4), id_o64, k > 0 ? 1u : joined);
+          mma_f16_ts(o_col + 64, p + k * 8, be + k * (2048 >> 4), id_o64, k > 0 ? 1u : joined);
         }
-        __syncwarp();
       }
-      return true;
     };
     bool ok = true;
     if (nt) {
-      ok = wait_warp(bar(ms.qfull[t]), 0, ctl) && k_landed(0);
-      if (ok) first(0);
-      for (int i = 0; ok && i < nt; ++i) {
-        // the tiles take turns, so that one's softmax falls under the other's products (left to themselves they
-        // run in step); what a turn needs is waited for before it
-        ok = v_landed(i) && wait_warp(bar(ms.pfull[t][0]), (uint32_t)i & 1u, ctl);
-        if (ok && two && (t ? i < n0 : i > 0))
-          ok = wait_warp(bar(ms.turn[t]), (uint32_t)(t ? i : i - 1) & 1u, ctl);
-        ok = ok && second(i);
-        if (ok && i + 1 < nt) {
-          ok = k_landed(i + 1);  // (not before the turn: the ring has no room for it much earlier)
-          if (ok) first(i + 1);
+      ok = wait_warp(bar(ms.qfull[t]), 0, ctl);
+      int s = 0;  // ring block of the next operand
+      // Turn i: the second product of key tile i, the first of i + 1 (turn -1: the first alone).  The tiles take
+      // turns, so that one's softmax falls under the other's products (left to themselves they run in step).
+      for (int i = -1; ok && i < nt; ++i) {
+        if (i >= 0) {
+          ok = wait_warp(bar(ms.vfull[i & 1]), (uint32_t)(i >> 1) & 1u, ctl) &&
+               wait_warp(bar(ms.pfull[t][0]), (uint32_t)i & 1u, ctl);
+          if (ok && two && (t ? i < n0 : i > 0))
+            ok = wait_warp(bar(ms.turn[t]), (uint32_t)(t ? i : i - 1) & 1u, ctl);
+#pragma unroll 1
+          for (int half = 0; ok && half < 2; ++half) {
+            if (half) ok = wait_warp(bar(ms.pfull[t][1]), (uint32_t)i & 1u, ctl);
+            if (!ok) break;
+            fence_after();
+            if (elect()) second(half, s, half || i > 0 ? 1u : 0u);
+            __syncwarp();
+          }
+          if (!ok) break;
+          if (elect()) {
+            commit(bar(ms.empty[s]));
+            commit(bar(ms.empty[(s + 1) % kRing]));
+            if (i + 1 == nt) commit(bar(ms.ofull[t]));
+          }
+          __syncwarp();
+          s = (s + kVBlocks) % kRing;
         }
-        if (ok && two && lane == 0) mbar_arrive(bar(ms.turn[t ^ 1]));
+        if (i + 1 < nt) {
+          ok = wait_warp(bar(ms.kfull[(i + 1) & 1]), (uint32_t)((i + 1) >> 1) & 1u, ctl);
+          if (!ok) break;
+          fence_after();
+#pragma unroll 1
+          for (int b = 0; b < kKBlocks; ++b) {
+            // (the turn goes on before its last instructions)
+            if (b == kKBlocks - 1 && two && i >= 0 && lane == 0) mbar_arrive(bar(ms.turn[t ^ 1]));
+            if (elect()) first(b, s);
+            __syncwarp();
+            s = (s + 1) % kRing;
+          }
+          if (elect()) commit(bar(ms.sfull[t]));
+          __syncwarp();
+        } else if (two && lane == 0) {
+          mbar_arrive(bar(ms.turn[t ^ 1]));
+        }
       }
     }
     // The blocks of key tiles that only the other row tile sees: handed back
@@ -621,7 +625,8 @@ __global__ void __launch_bounds__(kAttThreads, 1)
     // of the ring.
     if (t == 0 || two)
       for (int i = nt; ok && i < n; ++i) {
-        ok = k_landed(i) && v_landed(i);
+        ok = wait_warp(bar(ms.kfull[i & 1]), (uint32_t)(i >> 1) & 1u, ctl) &&
+             wait_warp(bar(ms.vfull[i & 1]), (uint32_t)(i >> 1) & 1u, ctl);
         if (ok && lane < kKV) mbar_arrive(bar(ms.empty[(kKV * i + lane) % kRing]));
       }
     if (elect()) commit(bar(ms.done[t]));
