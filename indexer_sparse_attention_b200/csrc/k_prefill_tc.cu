@@ -401,8 +401,7 @@ __device__ __forceinline__ int parts_of(int tail, int n) {
 struct AttMisc {
   uint64_t kfull[2], vfull[2];  // K(i), V(i) landed: barrier i % 2 (the ring holds less than two key tiles)
   uint64_t empty[kRing];
-  uint64_t qfull[2], sfull[2], pfull[2][2], ofull[2];
-  uint64_t turn[2];
+  uint64_t qfull[2], sfull[2][2], pfull[2][2], odone[2];
   uint64_t done[2];
   int64_t tmp[33];
   uint32_t tmem;
@@ -481,13 +480,13 @@ __global__ void __launch_bounds__(kAttThreads, 1)
     for (int t = 0; t < 2; ++t) {
       mbar_init(bar(ms.kfull[t]), 1);
       mbar_init(bar(ms.vfull[t]), 1);
-      mbar_init(bar(ms.turn[t]), 1);
       mbar_init(bar(ms.done[t]), 1);
       mbar_init(bar(ms.qfull[t]), 128);
-      mbar_init(bar(ms.sfull[t]), 1);
-      mbar_init(bar(ms.pfull[t][0]), 4);
-      mbar_init(bar(ms.pfull[t][1]), 4);
-      mbar_init(bar(ms.ofull[t]), 1);
+      for (int half = 0; half < 2; ++half) {
+        mbar_init(bar(ms.sfull[t][half]), 1);
+        mbar_init(bar(ms.pfull[t][half]), 4);
+      }
+      mbar_init(bar(ms.odone[t]), 1);
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -535,32 +534,32 @@ __global__ void __launch_bounds__(kAttThreads, 1)
       }
   } else if (warp > 8) {
     // ======================= MMA issue, a warp for each row tile =======================
-    // (One warp for both left the tensor cores idle while it waited: a wait
-    // that succeeds at once takes 75 cycles, and the pipe queues 2 to 4
-    // instructions of 64.)  The products of one tile need their order, those of
-    // the two tiles do not.
+    // The products of one tile need their order, those of the two tiles do not;
+    // while one warp waits (75 cycles even where all is there) the other's
+    // instructions run.
     const int t = warp - 9, nt = t ? n1 : n0;
-    const uint32_t id_s = idesc_bf16(128, 128, 0, 0);
+    const uint32_t id_s = idesc_bf16(128, 64, 0, 0);
     const uint32_t id_o = idesc_bf16(128, 128, 0, 1), id_o64 = idesc_bf16(128, 64, 0, 1);
     const uint32_t s_col = tmem + t * 128, o_col = tmem + kOCol + t * 128;
-    // ring blocks of K(i): 5 i .. + 2, of V(i): 5 i + 3, 5 i + 4
     const uint64_t ad = sw128_desc(q_at + t * kKBlocks * kBlk, 16, 1024);
-    // The elected lane's parts of a turn, in loops of four instructions: the
-    // warp shares its instruction cache with the softmax, and a turn written out
-    // took longer to fetch than to run.  S(i), 64 columns b of K at ring block s:
-    auto first = [&](int b, int s) {
-      const uint64_t aq = ad + (uint64_t)b * (kBlk >> 4), bd = sw128_desc(r_at + s * kBlk, 16, 1024);
-      const uint32_t joined = b > 0;
+    // The elected lane's parts, in loops of four instructions: the warp shares
+    // its instruction cache with the softmax.  S(j): 64 keys (half j % 2 of K at
+    // ring blocks s ..), columns b of K.
+    auto first = [&](int j, int b, int s) {
+      const uint32_t half = j & 1;
+      const uint64_t aq = ad + (uint64_t)b * (kBlk >> 4);
+      const uint64_t bd = sw128_desc(r_at + s * kBlk + half * (kBlk / 2), 16, 1024);
+      const uint32_t joined = b > 0, d = s_col + half * 64;
 #pragma unroll
-      for (int kk = 0; kk < 4; ++kk) mma_f16(s_col, aq + 2 * kk, bd + 2 * kk, id_s, kk > 0 ? 1u : joined);
-      commit(bar(ms.empty[s]));
+      for (int kk = 0; kk < 4; ++kk) mma_f16(d, aq + 2 * kk, bd + 2 * kk, id_s, kk > 0 ? 1u : joined);
+      if (half) commit(bar(ms.empty[s]));
     };
-    // O += P(i) V(i), 64 keys, V at ring blocks s, s + 1.  V's two blocks are one operand 128 wide (with N = 64 an
+    // O += P(j) V(j), V at ring blocks s, s + 1.  V's two blocks are one operand 128 wide (with N = 64 an
     // instruction takes as long), but where the ring ends between them.
-    auto second = [&](int half, int s, uint32_t joined) {
-      const uint64_t step = (uint64_t)half * (4 * 2048 >> 4);
-      const uint64_t bd = sw128_desc(r_at + s * kBlk, kBlk, 1024) + step, be = sw128_desc(r_at, kBlk, 1024) + step;
-      const uint32_t p = s_col + half * 32;
+    auto second = [&](int j, int s) {
+      const uint32_t half = j & 1, p = s_col + half * 64, joined = j > 0;
+      const uint64_t bd = sw128_desc(r_at + s * kBlk + half * (kBlk / 2), kBlk, 1024);
+      const uint64_t be = sw128_desc(r_at + half * (kBlk / 2), kBlk, 1024);
       if (s != kRing - 1) {
 #pragma unroll
         for (int k = 0; k < 4; ++k) mma_f16_ts(o_col, p + k * 8, bd + k * (2048 >> 4), id_o, k > 0 ? 1u : joined);
@@ -571,52 +570,38 @@ __global__ void __launch_bounds__(kAttThreads, 1)
           mma_f16_ts(o_col + 64, p + k * 8, be + k * (2048 >> 4), id_o64, k > 0 ? 1u : joined);
         }
       }
+      if (half) {
+        commit(bar(ms.empty[s]));
+        commit(bar(ms.empty[(s + 1) % kRing]));
+      }
+      commit(bar(ms.odone[t]));
     };
     bool ok = true;
     if (nt) {
       ok = wait_warp(bar(ms.qfull[t]), 0, ctl);
-      int s = 0;  // ring block of the next operand
-      // Turn i: the second product of key tile i, the first of i + 1 (turn -1: the first alone).  The tiles take
-      // turns, so that one's softmax falls under the other's products (left to themselves they run in step).
-      for (int i = -1; ok && i < nt; ++i) {
-        if (i >= 0) {
-          ok = wait_warp(bar(ms.vfull[i & 1]), (uint32_t)(i >> 1) & 1u, ctl) &&
-               wait_warp(bar(ms.pfull[t][0]), (uint32_t)i & 1u, ctl);
-          if (ok && two && (t ? i < n0 : i > 0))
-            ok = wait_warp(bar(ms.turn[t]), (uint32_t)(t ? i : i - 1) & 1u, ctl);
-#pragma unroll 1
-          for (int half = 0; ok && half < 2; ++half) {
-            if (half) ok = wait_warp(bar(ms.pfull[t][1]), (uint32_t)i & 1u, ctl);
-            if (!ok) break;
-            fence_after();
-            if (elect()) second(half, s, half || i > 0 ? 1u : 0u);
-            __syncwarp();
-          }
+      // step j: the second product of half j, the first of half j + 2, whose place in TMEM half j leaves
+      for (int j = -2; ok && j < 2 * nt; ++j) {
+        if (j >= 0) {
+          const int i = j >> 1;
+          ok = ((j & 1) || wait_warp(bar(ms.vfull[i & 1]), (uint32_t)(i >> 1) & 1u, ctl)) &&
+               wait_warp(bar(ms.pfull[t][j & 1]), (uint32_t)i & 1u, ctl);
           if (!ok) break;
-          if (elect()) {
-            commit(bar(ms.empty[s]));
-            commit(bar(ms.empty[(s + 1) % kRing]));
-            if (i + 1 == nt) commit(bar(ms.ofull[t]));
-          }
+          fence_after();
+          if (elect()) second(j, (kKV * i + kKBlocks) % kRing);
           __syncwarp();
-          s = (s + kVBlocks) % kRing;
         }
-        if (i + 1 < nt) {
-          ok = wait_warp(bar(ms.kfull[(i + 1) & 1]), (uint32_t)((i + 1) >> 1) & 1u, ctl);
+        if (j + 2 < 2 * nt) {
+          const int i = (j + 2) >> 1;
+          ok = (j & 1) || wait_warp(bar(ms.kfull[i & 1]), (uint32_t)(i >> 1) & 1u, ctl);
           if (!ok) break;
           fence_after();
 #pragma unroll 1
           for (int b = 0; b < kKBlocks; ++b) {
-            // (the turn goes on before its last instructions)
-            if (b == kKBlocks - 1 && two && i >= 0 && lane == 0) mbar_arrive(bar(ms.turn[t ^ 1]));
-            if (elect()) first(b, s);
+            if (elect()) first(j + 2, b, (kKV * i + b) % kRing);
             __syncwarp();
-            s = (s + 1) % kRing;
           }
-          if (elect()) commit(bar(ms.sfull[t]));
+          if (elect()) commit(bar(ms.sfull[t][j & 1]));
           __syncwarp();
-        } else if (two && lane == 0) {
-          mbar_arrive(bar(ms.turn[t ^ 1]));
         }
       }
     }
@@ -672,37 +657,43 @@ __global__ void __launch_bounds__(kAttThreads, 1)
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t s_at = tmem + lanes + t * 128, o_at = tmem + lanes + kOCol + t * 128;
     const int pos = pos0 + t * kRowTile + tid - i0 * kRowTile;  // this thread's row, from the part's first key
-    const int whole = (pos0 + t * kRowTile + 1) / kRowTile - i0;  // key tiles that every row of the tile sees whole
+    const int whole = (pos0 + t * kRowTile + 1) / 64 - 2 * i0;  // halves that every row of the tile sees whole
     const float scale = a.scale_log2;
     float m = -INFINITY, l = 0.f;
     bool ok = true;
-    for (int i = 0; i < nt; ++i) {
-      // (S of this tile follows the second product of the tile before: O is whole)
-      ok = wait_warp(bar(ms.sfull[t]), (uint32_t)i & 1u, ctl);
+    for (int j = 0; j < 2 * nt; ++j) {
+      const uint32_t at = s_at + (j & 1) * 64;
+      // (S of half j follows the second product of half j - 2)
+      ok = wait_warp(bar(ms.sfull[t][j & 1]), (uint32_t)(j >> 1) & 1u, ctl);
       if (!ok) break;
       fence_after();
-      uint32_t s[4][32];
-#pragma unroll
-      for (int c = 0; c < 4; ++c) tmem_ld32(s_at + c * 32, s[c]);
+      uint32_t s[2][32];
+      tmem_ld32(at, s[0]);
+      tmem_ld32(at + 32, s[1]);
       tmem_wait_ld();
-      if (i >= whole) {
-        const int left = pos - i * kRowTile;  // columns 0 .. left are seen
+      if (j >= whole) {
+        const int left = pos - j * 64;  // columns 0 .. left are seen
 #pragma unroll
-        for (int c = 0; c < 128; ++c)
+        for (int c = 0; c < 64; ++c)
           if (c > left) s[c >> 5][c & 31] = 0xff800000u;
       }
       float mt[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-      for (int c = 0; c < 32; ++c)
+      for (int c = 0; c < 32; c += 4)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) mt[k] = fmaxf(mt[k], __uint_as_float(s[k][c]));
+        for (int k = 0; k < 4; ++k)
+          mt[k] = max3(mt[k], __uint_as_float(s[0][c + k]), __uint_as_float(s[1][c + k]));
       const float top = fmaxf(fmaxf(mt[0], mt[1]), fmaxf(mt[2], mt[3])) * scale;
-      if (__any_sync(0xffffffffu, top > m + kLazy)) {  // (true at the first tile: m is -inf)
+      if (__any_sync(0xffffffffu, top > m + kLazy)) {  // (true at the first half: m is -inf)
         const float mn = fmaxf(m, top);
         const float f = mn == -INFINITY ? 1.f : ex2(m - mn);
         m = mn;
         l *= f;
-        if (i > 0) {
+        if (j > 0) {
+          // (the second product of half j - 2 is complete, S of half j follows it)
+          ok = wait_warp(bar(ms.odone[t]), (uint32_t)(j - 1) & 1u, ctl);
+          if (!ok) break;
+          fence_after();
 #pragma unroll 1
           for (int c = 0; c < 8; ++c) {
             uint32_t o[16];
@@ -716,26 +707,24 @@ __global__ void __launch_bounds__(kAttThreads, 1)
       }
       const float ref = m == -INFINITY ? 0.f : m;
       float sum[4] = {0.f, 0.f, 0.f, 0.f};
+      uint32_t p[32];
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        uint32_t p[32];
-#pragma unroll
-        for (int c = 0; c < 32; ++c) {
-          const int x = 64 * half + 2 * c;
-          const float p0 = ex2(fmaf(__uint_as_float(s[x >> 5][x & 31]), scale, -ref));
-          const float p1 = ex2(fmaf(__uint_as_float(s[x >> 5][(x & 31) + 1]), scale, -ref));
-          sum[c & 3] += p0 + p1;
-          p[c] = pack_bf16(p0, p1);
-        }
-        tmem_st32(s_at + half * 32, p);
-        tmem_wait_st();
-        fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(ms.pfull[t][half]));
+      for (int c = 0; c < 32; ++c) {
+        const int x = 2 * c;
+        const float p0 = ex2(fmaf(__uint_as_float(s[x >> 5][x & 31]), scale, -ref));
+        const float p1 = ex2(fmaf(__uint_as_float(s[x >> 5][(x & 31) + 1]), scale, -ref));
+        sum[c & 3] += p0 + p1;
+        p[c] = pack_bf16(p0, p1);
       }
+      tmem_st32(at, p);
+      tmem_wait_st();
+      fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(ms.pfull[t][j & 1]));
       l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
     }
-    if (ok && nt) ok = wait_warp(bar(ms.ofull[t]), 0, ctl);
+    // the last two second products, in order (parities tell only neighbours apart)
+    if (ok && nt) ok = wait_warp(bar(ms.odone[t]), 0, ctl) && wait_warp(bar(ms.odone[t]), 1, ctl);
     if (ok && w.parts > 1) {
       // a part: unnormalised, for the join
       const int64_t at = (int64_t)w.slot * 2 * kRowTile + t * kRowTile + tid;
