@@ -85,17 +85,14 @@ __global__ void __launch_bounds__(kThreads) k_attn_simt(const __grid_constant__ 
   t.p = t.kv + kT * t.stride;
   t.alpha = t.p + kNH * kT;
   int64_t* row = reinterpret_cast<int64_t*>(sm + ((t.alpha + kNH - sm + 1) / 2 * 2));  // [kT] cache rows, -1: none
-  __shared__ int tmp[35];
+  __shared__ int tmp[36];
   __shared__ float norm[kNH];
   const int g = blockIdx.x % a.ngroups, u = blockIdx.x / a.ngroups;
   const int h0 = g * kNH, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int items = a.Q * a.rows;
-  const int total = attn_units_before(a, items, tmp), ranges = min(a.ranges, total);
-  if (u >= ranges) return;
-  const int my_begin = range_begin(total, ranges, u), stop = range_begin(total, ranges, u + 1);
-  int first;
-  int item = attn_item_of(a, my_begin, tmp, &first);
-  int at = my_begin;
+  const Place at0 = attn_place(a, -1, u, tmp);
+  if (u >= at0.ranges) return;
+  const int my_begin = range_begin(at0.total, at0.ranges, u), stop = range_begin(at0.total, at0.ranges, u + 1);
+  int item = at0.item, first = at0.first, at = my_begin;
   while (at < stop) {
     const int q = item / a.rows, r = item - q * a.rows;
     const int end = attn_end(a, q, r);
@@ -124,9 +121,31 @@ __global__ void __launch_bounds__(kThreads) k_attn_simt(const __grid_constant__ 
         row[lane] = (slot >= 0 && slot < end) ? cache_row(C, q, slot, a.err) : -1;
       }
       __syncthreads();
-      for (int i = threadIdx.x; i < kT * W; i += kThreads) {
-        const int j = i / W, d = i - j * W;
-        t.kv[j * t.stride + d] = row[j] >= 0 ? to_f32(reinterpret_cast<const T*>(C.data)[row[j] * W + d]) : 0.f;
+      // a warp takes tokens warp, warp + 8, ..: all four of one piece in flight at once
+      constexpr int V = 16 / (int)sizeof(T);
+      const bool vec = ((uintptr_t)C.data & 15) == 0 && W % V == 0;
+      for (int d = lane * (vec ? V : 1); d < W; d += 32 * (vec ? V : 1)) {
+        uint4 x[kT / 8];
+#pragma unroll
+        for (int i = 0; i < kT / 8; ++i) {
+          const int64_t r = row[warp + 8 * i];
+          x[i] = make_uint4(0, 0, 0, 0);
+          if (r >= 0) {
+            const T* src = reinterpret_cast<const T*>(C.data) + r * W + d;
+            if (vec)
+              x[i] = *reinterpret_cast<const uint4*>(src);
+            else
+              *reinterpret_cast<T*>(&x[i]) = *src;
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < kT / 8; ++i) {
+          const T* e = reinterpret_cast<const T*>(&x[i]);
+          float* dst = t.kv + (warp + 8 * i) * t.stride + d;
+#pragma unroll
+          for (int k = 0; k < V; ++k)
+            if (vec || k == 0) dst[k] = to_f32(e[k]);
+        }
       }
       const bool seen = row[lane] >= 0;
       __syncthreads();
@@ -171,14 +190,14 @@ constexpr int kJoinWarps = 8;
 
 template <typename T, int WPH>
 __global__ void __launch_bounds__(kJoinWarps * 32) k_attn_combine(const __grid_constant__ AttnArgs a) {
-  __shared__ int tmp[35];
+  __shared__ int tmp[36];
   __shared__ float4 sums[WPH > 1 ? kJoinWarps : 1][WPH > 1 ? 128 : 1];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int item = a.whole * a.ranges + blockIdx.y, h = blockIdx.x * (kJoinWarps / WPH) + warp / WPH, mine = warp % WPH;
   // The lengths were there before the attention kernel started, so the place
   // of the shares is found while it still runs.
-  const int total = attn_units_before(a, a.Q * a.rows, tmp), ranges = min(a.ranges, total);
-  const int first = attn_units_before(a, item, tmp);
+  const Place at = attn_place(a, item, 0, tmp);
+  const int total = at.total, ranges = at.ranges, first = at.first;
   const int n = attn_tiles(a, attn_end(a, item / a.rows, item % a.rows));
   const int u0 = range_of(total, ranges, first), u1 = range_of(total, ranges, first + n - 1);
   pdl_enter();
@@ -438,7 +457,7 @@ cudaError_t launch_attn_simt(const AttnArgs& a, int bf16, cudaStream_t s) {
 cudaError_t launch_attn_combine(const AttnArgs& a, int bf16, cudaStream_t s) {
   // an item's shares, at the even lengths of lists: a few for many items, else many
   const int items = a.Q * a.rows - a.whole * a.ranges;
-  const bool many = a.ranges > 12 * items;
+  const bool many = a.rest > 12 * items;
   const int per = many ? 1 : kJoinWarps;
   auto kernel = many ? (bf16 ? k_attn_combine<__nv_bfloat16, kJoinWarps> : k_attn_combine<float, kJoinWarps>)
                      : (bf16 ? k_attn_combine<__nv_bfloat16, 1> : k_attn_combine<float, 1>);

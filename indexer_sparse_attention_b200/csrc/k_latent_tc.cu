@@ -178,15 +178,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   // the block's items and units (all threads)
   Walk w;
   {
-    int* tmp = reinterpret_cast<int*>(ms.info);
-    const int total = attn_units_before(a, a.Q * a.rows, tmp), ranges = min(a.ranges, total);
+    const Place at = attn_place(a, -1, u, reinterpret_cast<int*>(ms.info));
     w.whole = a.whole;
-    w.later = 0;
-    w.at = w.stop = w.first = 0;
-    if (u < ranges) {
-      w.at = range_begin(total, ranges, u);
-      w.stop = range_begin(total, ranges, u + 1);
-      w.later = attn_item_of(a, w.at, tmp, &w.first);
+    w.later = at.item;
+    w.first = at.first;
+    w.at = w.stop = 0;
+    if (u < at.ranges) {
+      w.at = range_begin(at.total, at.ranges, u);
+      w.stop = range_begin(at.total, at.ranges, u + 1);
     }
     w.item = w.whole ? u * w.whole : w.later;
     __syncthreads();

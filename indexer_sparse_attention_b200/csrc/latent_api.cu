@@ -328,18 +328,39 @@ spin_status spin_latent_attention(spin_latent lt, int rows, const void* cache, i
     const int64_t n = a.list ? a.topk : a.max_slots;
     a.ranges = (int)std::min<int64_t>(std::max(1, blocks / a.ngroups), (int64_t)a.Q * rows * ((n + tile - 1) / tile));
     a.whole = 0;
+    a.rest = a.ranges;
   };
   cudaError_t e;
   if (attn_tc_supported(a, bf16)) {
     const int groups = (a.H + kTcHeads - 1) / kTcHeads;
     plan(kTcTile, ((a.H + groups - 1) / groups + 15) / 16 * 16, std::min(lt->sms, kTcBlocks));
-    if (a.list) a.whole = a.Q * rows / a.ranges;
+    if (a.list) {
+      // Equally long items: as many whole ones as go round, then the others
+      //   a block each,
+      //   or cut evenly, `cut` blocks each (the join costs about as much as 2 tiles),
+      //   or as one run of units over all blocks (and blocks that change items, about 5 tiles),
+      // whichever ends first.  128 items of 32 tiles on 148 blocks: 73 us as one run, 61 us a block each.
+      const int items = a.Q * rows, per = (a.topk + kTcTile - 1) / kTcTile;
+      a.whole = items / a.ranges;
+      const int left = items - a.whole * a.ranges;
+      if (left) {
+        const int cut = std::min(a.ranges / left, per);
+        const int even = cut > 1 ? (per + cut - 1) / cut + 2 : per;
+        const int run = (int)((int64_t)left * per / a.ranges) + 5;
+        if (even <= run) a.rest = left * cut;
+        if (a.rest == left && a.whole == 0) {  // a block each
+          a.ranges = left;
+          a.whole = 1;
+        }
+      }
+    }
     e = launch_attn_tc(a, (cudaStream_t)stream);
   } else {
     plan(kSimtTile, kSimtHeads, std::min(2 * lt->sms, kSimtBlocks));
     e = launch_attn_simt(a, bf16, (cudaStream_t)stream);
   }
-  if (e == cudaSuccess && a.whole * a.ranges < a.Q * rows) e = launch_attn_combine(a, bf16, (cudaStream_t)stream);
+  const int left = a.Q * rows - a.whole * a.ranges;  // items that may lie in several blocks' ranges
+  if (e == cudaSuccess && left && !(a.list && a.rest == left)) e = launch_attn_combine(a, bf16, (cudaStream_t)stream);
   return cuda_status(e);
 }
 

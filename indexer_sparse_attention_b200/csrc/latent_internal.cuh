@@ -114,6 +114,7 @@ struct AttnArgs {
   int ngroups;               // ceil(H / group)
   int ranges;                // blocks per head group, at most
   int whole;                 // items that each block takes whole (lists only)
+  int rest;                  // of the blocks, those that share the other items, at most
   float* part;               // [ngroups * ranges * 2][group][dc] unnormalised outputs
   float2* part_ml;           // [ngroups * ranges * 2][group] (maximum in log2 units, sum)
 };
@@ -129,51 +130,6 @@ __device__ __forceinline__ int attn_tiles(const AttnArgs& a, int end) {
   return n > 0 ? (n + a.tile - 1) / a.tile : 1;
 }
 
-// Units of the items that are not taken whole, before `item` (Q * rows: all
-// of them), summed by all threads of the block; tmp: 35 ints of shared memory.  The host has checked that all units
-// together fit 31 bits.
-__device__ __forceinline__ int attn_units_before(const AttnArgs& a, int item, int* tmp) {
-  if (a.list) return (item - a.whole * a.ranges) * ((a.topk + a.tile - 1) / a.tile);
-  int sum = 0;
-  for (int i = threadIdx.x; i < item; i += blockDim.x) sum += attn_tiles(a, attn_end(a, i / a.rows, i % a.rows));
-#pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  if ((threadIdx.x & 31) == 0) tmp[threadIdx.x >> 5] = sum;
-  __syncthreads();
-  sum = 0;
-  for (int w = 0; w < (int)(blockDim.x + 31) / 32; ++w) sum += tmp[w];
-  __syncthreads();
-  return sum;
-}
-
-// The item that holds unit g, and that item's first unit (all threads of the
-// block; tmp as above).
-__device__ __forceinline__ int attn_item_of(const AttnArgs& a, int g, int* tmp, int* first) {
-  if (a.list) {
-    const int per = (a.topk + a.tile - 1) / a.tile;
-    *first = g / per * per;
-    return a.whole * a.ranges + g / per;
-  }
-  const int items = a.Q * a.rows;
-  int carry = 0;
-  for (int base = 0; base < items && carry <= g; base += blockDim.x) {
-    const int i = base + (int)threadIdx.x;
-    const int n = i < items ? attn_tiles(a, attn_end(a, i / a.rows, i % a.rows)) : 0;
-    int tot;
-    const int at = carry + block_exclusive_scan(n, tmp, &tot);
-    if (at <= g && g < at + n) {
-      tmp[33] = i;
-      tmp[34] = at;
-    }
-    carry += tot;
-  }
-  __syncthreads();
-  const int item = tmp[33];
-  *first = tmp[34];
-  __syncthreads();
-  return item;
-}
-
 // First unit of range u of `ranges` over `total` >= ranges units, and the
 // range that holds unit g.
 __host__ __device__ __forceinline__ int range_begin(int total, int ranges, int u) {
@@ -182,6 +138,68 @@ __host__ __device__ __forceinline__ int range_begin(int total, int ranges, int u
 __host__ __device__ __forceinline__ int range_of(int total, int ranges, int g) {
   // begin(u) <= g  <=>  total u < (g + 1) ranges
   return (int)(((int64_t)(g + 1) * ranges - 1) / total);
+}
+
+// The units of the items that are not taken whole: how many there are and over
+// how many ranges they go, the item asked for and its first unit.
+struct Place {
+  int total, ranges;
+  int item, first;
+};
+
+// Places either `item`, or (item < 0) the item that holds the first unit of
+// range u (item 0 where there is no such range).  All threads of the block; tmp:
+// 36 ints of shared memory.  The host has checked that all units together fit
+// 31 bits.
+__device__ __forceinline__ Place attn_place(const AttnArgs& a, int item, int u, int* tmp) {
+  const int items = a.Q * a.rows;
+  Place p;
+  if (a.list) {
+    const int per = (a.topk + a.tile - 1) / a.tile, base = a.whole * a.ranges;
+    p.total = (items - base) * per;
+    p.ranges = min(a.rest, p.total);
+    const int i = item >= 0 ? item - base : u < p.ranges ? range_begin(p.total, p.ranges, u) / per : 0;
+    p.item = base + i;
+    p.first = i * per;
+    return p;
+  }
+  // every item's tiles, one after the other
+  auto tiles = [&](int i) { return i < items ? attn_tiles(a, attn_end(a, i / a.rows, i % a.rows)) : 0; };
+  int n = 0, at = 0;
+  if (items <= (int)blockDim.x) {
+    n = tiles(threadIdx.x);
+    at = block_exclusive_scan(n, tmp, &p.total);
+  } else {
+    int sum = 0;
+    for (int i = threadIdx.x; i < items; i += blockDim.x) sum += tiles(i);
+    block_exclusive_scan(sum, tmp, &p.total);
+  }
+  p.ranges = min(a.rest, p.total);
+  const int want = item >= 0 || u >= p.ranges ? 0 : range_begin(p.total, p.ranges, u);
+  auto found = [&](int i, int n, int at) {
+    if (item >= 0 ? i == item : at <= want && want < at + n) {
+      tmp[33] = i;
+      tmp[34] = at;
+    }
+  };
+  if (items <= (int)blockDim.x) {
+    found(threadIdx.x, n, at);
+  } else {
+    int carry = 0;
+    for (int base = 0; base < items; base += blockDim.x) {
+      const int i = base + (int)threadIdx.x, m = tiles(i);
+      int tot;
+      const int ex = block_exclusive_scan(m, tmp, &tot);
+      found(i, m, carry + ex);
+      carry += tot;
+      if (item >= 0 ? base + (int)blockDim.x > item : carry > want) break;
+    }
+  }
+  __syncthreads();
+  p.item = tmp[33];
+  p.first = tmp[34];
+  __syncthreads();
+  return p;
 }
 
 // Cache row (page * b + place) of a slot, or -1 where the slot is not one

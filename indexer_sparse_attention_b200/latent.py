@@ -92,12 +92,22 @@ class SpinLatent:
         self.dtype = torch.bfloat16 if cfg.dtype == isa.SPIN_BF16 else torch.float32
         self.mem = torch.empty(nbytes + 256, dtype=torch.uint8, device=device)
         self.device = self.mem.device
+        self._derive()
         off = (-self.mem.data_ptr()) % 256
         self.base = self.mem[off:off + nbytes]
         h = _vp()
         isa._check(lib.spin_latent_create(ctypes.byref(cfg), _vp(self.base.data_ptr()), nbytes,
                                           _stream(self, stream), ctypes.byref(h)), "spin_latent_create")
         self.handle = h
+
+    def _derive(self):
+        """What the calls' checks compare with, taken from the config once."""
+        c = self.cfg
+        self.index = -1 if self.device.type == "cpu" else self.device.index
+        self.requests, self.heads, self.latent, self.rope = c.num_requests, c.num_heads, c.latent_dim, c.rope_dim
+        self.page = (c.block_size, c.latent_dim + c.rope_dim)
+        self.blocks = -(-c.max_slots // c.block_size)
+        self.per_request = (c.num_requests,)
 
     def close(self):
         if getattr(self, "handle", None) is not None and self.handle.value:
@@ -113,61 +123,60 @@ class SpinLatent:
 
 def _stream(lt: SpinLatent, stream) -> int:
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(lt.device.index)
+        return torch._C._cuda_getCurrentRawStream(lt.index)
     if stream.device != lt.device:
         raise ValueError(f"the stream is on {stream.device}, the handle on {lt.device}")
     return stream.cuda_stream
 
 
-def _place(lt: SpinLatent, t: torch.Tensor, name: str, dtype) -> None:
+# Each check is one expression where everything is as it should be (these run
+# in every call), and the reason is looked for only where it is not.
+def _refuse(lt: SpinLatent, t: torch.Tensor, name: str, dtype, shape: tuple):
     if t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.device != lt.device:
+    if t.get_device() != lt.index:
         raise ValueError(f"{name} must be on {lt.device}, got {t.device}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have the shape {tuple(shape)}, got {tuple(t.shape)}")
+    raise ValueError(f"{name} must be contiguous")
 
 
 def _dense(lt: SpinLatent, t: Optional[torch.Tensor], name: str, dtype, shape: tuple) -> Optional[int]:
     """The address of a contiguous tensor of exactly this shape (None: a NULL pointer)."""
     if t is None:
         return None
-    _place(lt, t, name, dtype)
-    if t.shape != shape:
-        raise ValueError(f"{name} must have the shape {shape}, got {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    if t.dtype is dtype and t.get_device() == lt.index and t.shape == shape and t.is_contiguous():
+        return t.data_ptr()
+    _refuse(lt, t, name, dtype, shape)
 
 
 def _tokens(lt: SpinLatent, t: torch.Tensor, name: str, shape: tuple):
     """(address, token stride, head stride) of a tensor [Q, rows, (heads,) width] whose tokens lie at one stride."""
-    _place(lt, t, name, lt.dtype)
-    if t.shape != shape:
-        raise ValueError(f"{name} must have the shape {shape}, got {tuple(t.shape)}")
     st = t.stride()
+    if t.dtype is not lt.dtype or t.get_device() != lt.index or t.shape != shape:
+        _refuse(lt, t, name, lt.dtype, shape)
     if st[-1] != 1:
         raise ValueError(f"the last dimension of {name} must be contiguous")
-    Q, rows = shape[:2]
+    Q, rows = shape[0], shape[1]
     if rows > 1:
-        if Q > 1 and st[0] != rows * st[1]:
-            raise ValueError(f"the rows of all requests of {name} must lie at one stride")
         token = st[1]
+        if Q > 1 and st[0] != rows * token:
+            raise ValueError(f"the rows of all requests of {name} must lie at one stride")
     else:
         token = st[0] if Q > 1 else 0
     return t.data_ptr(), token, st[2] if len(shape) == 4 and shape[2] > 1 else 0
 
 
 def _cache(lt: SpinLatent, cache: torch.Tensor, block_table: torch.Tensor):
-    c = lt.cfg
     if cache.dim() != 3:
         raise ValueError("cache must have the shape (pages, block_size, latent_dim + rope_dim)")
     if block_table.dim() != 2:
         raise ValueError("block_table must have the shape (num_requests, blocks)")
     pages, columns = cache.shape[0], block_table.shape[1]
-    blocks = -(-c.max_slots // c.block_size)
-    if columns < blocks:
-        raise ValueError(f"block_table must have at least {blocks} columns, got {columns}")
-    return (_dense(lt, cache, "cache", lt.dtype, (pages, c.block_size, c.latent_dim + c.rope_dim)), pages,
-            _dense(lt, block_table, "block_table", torch.int32, (c.num_requests, columns)), columns)
+    if columns < lt.blocks:
+        raise ValueError(f"block_table must have at least {lt.blocks} columns, got {columns}")
+    return (_dense(lt, cache, "cache", lt.dtype, (pages, *lt.page)), pages,
+            _dense(lt, block_table, "block_table", torch.int32, (lt.requests, columns)), columns)
 
 
 def _overlap(a: torch.Tensor, b: torch.Tensor) -> bool:
@@ -197,23 +206,28 @@ def spin_rope(lt: SpinLatent, x: torch.Tensor, positions: torch.Tensor, offset: 
     shape = x.shape
     if len(shape) != 3 or out.shape != shape:
         raise ValueError("x and out must have one shape (tokens, heads, head_dim)")
-    _place(lt, x, "x", lt.dtype)
+    if x.dtype is not lt.dtype or x.get_device() != lt.index:
+        _refuse(lt, x, "x", lt.dtype, shape)
     tokens, heads, width = shape
     sx = x.stride()
     xt, xh = sx[0] if tokens > 1 else 0, sx[1] if heads > 1 else 0
     if out is x:
         so, ot, oh = sx, xt, xh
     else:
-        _place(lt, out, "out", lt.dtype)
+        if out.dtype is not lt.dtype or out.get_device() != lt.index:
+            _refuse(lt, out, "out", lt.dtype, shape)
         so = out.stride()
         ot, oh = so[0] if tokens > 1 else 0, so[1] if heads > 1 else 0
     if sx[2] != 1 or so[2] != 1:
         raise ValueError("the last dimension of x and out must be contiguous")
-    # heads of out one behind the other in either order: the inner ones do not reach the next outer one
-    lo, hi = sorted((s, n) for s, n in ((ot, tokens), (oh, heads)) if n > 1) if tokens > 1 < heads else \
-        ((max(ot, oh), 1), (max(ot, oh), max(tokens, heads)))
-    if (lo[1] > 1 and lo[0] < width) or (hi[1] > 1 and hi[0] < lo[0] * (lo[1] - 1) + width):
-        raise ValueError("the heads of out must not overlap")
+    # heads of out one behind the other, in either order of tokens and heads
+    if not (oh >= width and ot >= oh * (heads - 1) + width):
+        steps = sorted((n_s[1], n_s[0]) for n_s in ((tokens, ot), (heads, oh)) if n_s[0] > 1)
+        reach = width
+        for step, n in steps:
+            if step < reach:
+                raise ValueError("the heads of out must not overlap")
+            reach += step * (n - 1)
     if out is not x and (out.data_ptr() != x.data_ptr() or ot != xt or oh != xh) and _overlap(x, out):
         raise ValueError("out must be x or not overlap it")
     _call("spin_rope", lt.handle, tokens, heads, width, offset, x.data_ptr(), xt, xh,
@@ -226,12 +240,10 @@ def spin_latent_append(lt: SpinLatent, rows: int, c: torch.Tensor, k_rope: torch
                        stream=None) -> None:
     """Writes c [Q, rows, latent_dim] and the rotated k_rope [Q, rows,
     rope_dim] into slots ctx_len - 1 .. of each request."""
-    cfg = lt.cfg
-    Q = cfg.num_requests
-    cp, ct, _ = _tokens(lt, c, "c", (Q, rows, cfg.latent_dim))
-    kp, kt, _ = _tokens(lt, k_rope, "k_rope", (Q, rows, cfg.rope_dim))
+    cp, ct, _ = _tokens(lt, c, "c", (lt.requests, rows, lt.latent))
+    kp, kt, _ = _tokens(lt, k_rope, "k_rope", (lt.requests, rows, lt.rope))
     _call("spin_latent_append", lt.handle, rows, cp, ct, kp, kt, *_cache(lt, cache, block_table),
-          _dense(lt, ctx_len, "ctx_len", torch.int32, (Q,)), _dense(lt, row_count, "row_count", torch.int32, (Q,)),
+          _dense(lt, ctx_len, "ctx_len", torch.int32, lt.per_request), _dense(lt, row_count, "row_count", torch.int32, lt.per_request),
           _stream(lt, stream))
 
 
@@ -243,13 +255,13 @@ def spin_latent_attention(lt: SpinLatent, rows: int, cache: torch.Tensor, block_
     rows, H, rope_dim] over the slots that topk [Q, rows, k] lists (None: all
     visible ones) into out [Q, rows, H, latent_dim] and lse [Q, rows, H]."""
     cfg = lt.cfg
-    Q, H = cfg.num_requests, cfg.num_heads
-    ql = _tokens(lt, q_latent, "q_latent", (Q, rows, H, cfg.latent_dim))
-    qr = _tokens(lt, q_rope, "q_rope", (Q, rows, H, cfg.rope_dim))
+    Q, H = lt.requests, lt.heads
+    ql = _tokens(lt, q_latent, "q_latent", (Q, rows, H, lt.latent))
+    qr = _tokens(lt, q_rope, "q_rope", (Q, rows, H, lt.rope))
     _call("spin_latent_attention", lt.handle, rows, *_cache(lt, cache, block_table), *ql, *qr,
-          _dense(lt, ctx_len, "ctx_len", torch.int32, (Q,)),
+          _dense(lt, ctx_len, "ctx_len", torch.int32, lt.per_request),
           _dense(lt, topk, "topk", torch.int32, (Q, rows, cfg.topk)),
-          _dense(lt, out, "out", lt.dtype, (Q, rows, H, cfg.latent_dim)),
+          _dense(lt, out, "out", lt.dtype, (Q, rows, H, lt.latent)),
           _dense(lt, lse, "lse", torch.float32, (Q, rows, H)), _stream(lt, stream))
 
 
@@ -265,7 +277,7 @@ def spin_latent_prefill(lt: SpinLatent, rows: int, cache: torch.Tensor, block_ta
     qp = _tokens(lt, q, "q", (Q, rows, H, cfg.nope_dim + cfg.rope_dim))
     _call("spin_latent_prefill", lt.handle, rows, *_cache(lt, cache, block_table), *qp,
           _dense(lt, w_kv, "w_kv", lt.dtype, (H, cfg.nope_dim + cfg.v_dim, cfg.latent_dim)),
-          _dense(lt, ctx_len, "ctx_len", torch.int32, (Q,)), _dense(lt, row_count, "row_count", torch.int32, (Q,)),
+          _dense(lt, ctx_len, "ctx_len", torch.int32, lt.per_request), _dense(lt, row_count, "row_count", torch.int32, lt.per_request),
           _dense(lt, out, "out", lt.dtype, (Q, rows, H, cfg.v_dim)), _stream(lt, stream))
 
 

@@ -86,6 +86,7 @@ class _NoHandle:
 
     def __init__(self, cfg, dtype=torch.bfloat16):
         self.cfg, self.dtype, self.device, self.handle = cfg, dtype, torch.device("cpu"), None
+        isa.SpinLatent._derive(self)
 
 
 def _args(cfg, rows=2, dtype=torch.bfloat16):
