@@ -498,13 +498,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(B.sfree[tile & 1]));
         }
-        // ---- weights by the reference that there is; where a row outgrew it (the first tile always), it moves
-        // and they are taken again ----
+        // ---- weights by the reference that there is; where a row outgrew it, it moves and they are taken again ----
         float d0, d1;
         for (int pass = 0;; ++pass) {
-          bool grow = false;
+          bool grow = flags & 1;  // (the first tile: there is no reference yet)
           d0 = d1 = 0.f;
-          if (ok && mine) {
+          if (ok && mine && (pass || !(flags & 1))) {
             const float r0 = m0 == -INFINITY ? 0.f : m0, r1 = m1 == -INFINITY ? 0.f : m1;
             float x0 = -INFINITY, x1 = -INFINITY;
 #pragma unroll

@@ -131,13 +131,17 @@ __device__ __forceinline__ int attn_tiles(const AttnArgs& a, int end) {
 }
 
 // First unit of range u of `ranges` over `total` >= ranges units, and the
-// range that holds unit g.
-__host__ __device__ __forceinline__ int range_begin(int total, int ranges, int u) {
-  return (int)((int64_t)total * u / ranges);
+// range that holds unit g.  (A division of 64 bits takes hundreds of cycles; most
+// products fit 32.)
+__device__ __forceinline__ int div_units(uint64_t n, int d) {
+  return n >> 32 ? (int)(n / (uint32_t)d) : (int)((uint32_t)n / (uint32_t)d);
 }
-__host__ __device__ __forceinline__ int range_of(int total, int ranges, int g) {
+__device__ __forceinline__ int range_begin(int total, int ranges, int u) {
+  return div_units((uint64_t)total * (uint32_t)u, ranges);
+}
+__device__ __forceinline__ int range_of(int total, int ranges, int g) {
   // begin(u) <= g  <=>  total u < (g + 1) ranges
-  return (int)(((int64_t)(g + 1) * ranges - 1) / total);
+  return div_units((uint64_t)(g + 1) * (uint32_t)ranges - 1, total);
 }
 
 // The units of the items that are not taken whole: how many there are and over
@@ -165,35 +169,46 @@ __device__ __forceinline__ Place attn_place(const AttnArgs& a, int item, int u, 
   }
   // every item's tiles, one after the other
   auto tiles = [&](int i) { return i < items ? attn_tiles(a, attn_end(a, i / a.rows, i % a.rows)) : 0; };
-  int n = 0, at = 0;
-  if (items <= (int)blockDim.x) {
-    n = tiles(threadIdx.x);
-    at = block_exclusive_scan(n, tmp, &p.total);
-  } else {
-    int sum = 0;
-    for (int i = threadIdx.x; i < items; i += blockDim.x) sum += tiles(i);
-    block_exclusive_scan(sum, tmp, &p.total);
+  if (items <= 128) {
+    // each warp by itself, four items a lane: no barriers
+    const int lane = threadIdx.x & 31;
+    int n[4], sum = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) sum += n[k] = tiles(4 * lane + k);
+    const int up = warp_inclusive_scan(sum);
+    p.total = __shfl_sync(0xffffffffu, up, 31);
+    p.ranges = min(a.rest, p.total);
+    const int want = item >= 0 || u >= p.ranges ? 0 : range_begin(p.total, p.ranges, u);
+    int at = up - sum, here = -1, start = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (item >= 0 ? 4 * lane + k == item : at <= want && want < at + n[k]) {
+        here = 4 * lane + k;
+        start = at;
+      }
+      at += n[k];
+    }
+    const int src = __ffs(__ballot_sync(0xffffffffu, here >= 0)) - 1;
+    p.item = __shfl_sync(0xffffffffu, here, src);
+    p.first = __shfl_sync(0xffffffffu, start, src);
+    return p;
   }
+  int sum = 0;
+  for (int i = threadIdx.x; i < items; i += blockDim.x) sum += tiles(i);
+  block_exclusive_scan(sum, tmp, &p.total);
   p.ranges = min(a.rest, p.total);
   const int want = item >= 0 || u >= p.ranges ? 0 : range_begin(p.total, p.ranges, u);
-  auto found = [&](int i, int n, int at) {
-    if (item >= 0 ? i == item : at <= want && want < at + n) {
+  int carry = 0;
+  for (int base = 0; base < items; base += blockDim.x) {
+    const int i = base + (int)threadIdx.x, m = tiles(i);
+    int tot;
+    const int at = carry + block_exclusive_scan(m, tmp, &tot);
+    if (item >= 0 ? i == item : at <= want && want < at + m) {
       tmp[33] = i;
       tmp[34] = at;
     }
-  };
-  if (items <= (int)blockDim.x) {
-    found(threadIdx.x, n, at);
-  } else {
-    int carry = 0;
-    for (int base = 0; base < items; base += blockDim.x) {
-      const int i = base + (int)threadIdx.x, m = tiles(i);
-      int tot;
-      const int ex = block_exclusive_scan(m, tmp, &tot);
-      found(i, m, carry + ex);
-      carry += tot;
-      if (item >= 0 ? base + (int)blockDim.x > item : carry > want) break;
-    }
+    carry += tot;
+    if (item >= 0 ? base + (int)blockDim.x > item : carry > want) break;
   }
   __syncthreads();
   p.item = tmp[33];
