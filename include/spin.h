@@ -527,7 +527,7 @@ SPIN_API spin_status spin_rope(spin_latent lt, int64_t tokens, int heads, int he
  * stay as they are.  block_table [Q][bt_stride] as for the indexer.  A
  * request with ctx_len < 1, a row_count outside 0..rows or a last slot past
  * max_slots sets ERR_CTX_LEN (bit 0) or ERR_ACCEPTED (bit 2) and writes
- * nothing; a page outside the cache sets ERR_PAGE (bit 1) and that token is
+ * nothing (with row_count 0 its ctx_len is not looked at); a page outside the cache sets ERR_PAGE (bit 1) and that token is
  * not written.  Two rows that share a slot of one page leave either's entry. */
 SPIN_API spin_status spin_latent_append(spin_latent lt, int rows, const void* c_dev, int64_t c_token_stride,
                                         const void* kr_dev, int64_t kr_token_stride, void* cache, int32_t num_pages,
@@ -556,7 +556,8 @@ SPIN_API spin_status spin_latent_attention(spin_latent lt, int rows, const void*
 
 /* Expanded attention of a chunk of new tokens over the paged context that
  * holds them already (spin_latent_append).  Rows r < row_count_dev[q] (NULL:
- * rows) of request q attend to slots 0..p_r.
+ * rows) of request q attend to slots 0..p_r; with row_count 0 the request's
+ * ctx_len is not looked at.
  *   q [Q][rows][num_heads][nope_dim + rope_dim], the last rope_dim elements
  *   rotated, with element strides between tokens and heads;
  *   w_kv [num_heads][nope_dim + v_dim][latent_dim] contiguous: W_uk then W_uv

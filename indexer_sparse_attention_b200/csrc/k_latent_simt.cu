@@ -208,6 +208,20 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_attn_combine(const __grid_c
   auto slot = [&](int u) {
     return ((int64_t)(u * a.ngroups + g) * 2 + (u == u0 ? head : 0)) * a.group + hh;
   };
+  // columns 4 (lane + 32 i) .. + 3 of kAhead shares at a time; the first ones' loads go out before the weights are
+  // known
+  constexpr int kAhead = 4;
+  float4 x[4][kAhead];
+  auto fetch = [&](int v) {
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      const float4* src = reinterpret_cast<const float4*>(a.part + slot(min(v + k * WPH, u1)) * dc);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (4 * (lane + 32 * i) < dc) x[i][k] = src[lane + 32 * i];
+    }
+  };
+  fetch(u0 + mine);
   float m = kNegInf;
   for (int u = u0 + lane; u <= u1; u += 32) m = fmaxf(m, a.part_ml[slot(u)].x);
 #pragma unroll
@@ -223,42 +237,35 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_attn_combine(const __grid_c
   const float norm = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
   if (mine == 0 && lane == 0 && a.lse)
     a.lse[(int64_t)item * a.H + h] = l == 0.f ? kNegInf : (m + log2f(l)) * (1.f / kLog2e);
-  // columns 4 (lane + 32 i) .. + 3
   float4 o[4] = {};
-  constexpr int kAhead = 4;
   for (int v = u0 + mine; v <= u1; v += WPH * kAhead) {
-    float wt[kAhead];
-    const float4* src[kAhead];
+    if (v != u0 + mine) fetch(v);
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) {
       const int u = v + k * WPH;
-      const int64_t at = slot(min(u, u1));
-      wt[k] = u <= u1 ? exp2f(a.part_ml[at].x - ref) : 0.f;
-      src[k] = reinterpret_cast<const float4*>(a.part + at * dc);
-    }
+      const float w = u <= u1 ? exp2f(a.part_ml[slot(u)].x - ref) : 0.f;
+      if (w == 0.f) continue;  // (a share without weight may hold anything)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int c = lane + 32 * i;
-      if (4 * c < dc) {
-        float4 x[kAhead];
-#pragma unroll
-        for (int k = 0; k < kAhead; ++k) x[k] = wt[k] != 0.f ? src[k][c] : make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int k = 0; k < kAhead; ++k) {
-          o[i].x = fmaf(wt[k], x[k].x, o[i].x);
-          o[i].y = fmaf(wt[k], x[k].y, o[i].y);
-          o[i].z = fmaf(wt[k], x[k].z, o[i].z);
-          o[i].w = fmaf(wt[k], x[k].w, o[i].w);
-        }
+      for (int i = 0; i < 4; ++i) {
+        o[i].x = fmaf(w, x[i][k].x, o[i].x);
+        o[i].y = fmaf(w, x[i][k].y, o[i].y);
+        o[i].z = fmaf(w, x[i][k].z, o[i].z);
+        o[i].w = fmaf(w, x[i][k].w, o[i].w);
       }
     }
   }
+  const bool aligned = ((uintptr_t)a.out & 15) == 0;
   auto store = [&](int c, float4 x) {
+    struct alignas(4 * sizeof(T)) Four {
+      T v[4];
+    } f{{from_f32<T>(x.x * norm), from_f32<T>(x.y * norm), from_f32<T>(x.z * norm), from_f32<T>(x.w * norm)}};
     T* out = reinterpret_cast<T*>(a.out) + ((int64_t)item * a.H + h) * dc + 4 * c;
-    out[0] = from_f32<T>(x.x * norm);
-    out[1] = from_f32<T>(x.y * norm);
-    out[2] = from_f32<T>(x.z * norm);
-    out[3] = from_f32<T>(x.w * norm);
+    if (aligned) {
+      *reinterpret_cast<Four*>(out) = f;
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) out[k] = f.v[k];
+    }
   };
   if constexpr (WPH == 1) {
 #pragma unroll

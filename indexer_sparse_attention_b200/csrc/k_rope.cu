@@ -131,6 +131,7 @@ __global__ void __launch_bounds__(256) k_append_vec(const __grid_constant__ Appe
       if (r == 0 && lane == 0) raise_error(a.err, ERR_ACCEPTED, q, (uint32_t)count);
       continue;
     }
+    if (count == 0) continue;  // (an idle request's ctx_len is not looked at)
     if (ctx < 1 || (int64_t)ctx - 1 + count > a.max_slots) {
       if (r == 0 && lane == 0) raise_error(a.err, ERR_CTX_LEN, q, (uint32_t)ctx);
       continue;
@@ -189,6 +190,7 @@ __global__ void __launch_bounds__(256) k_append(const __grid_constant__ AppendAr
       if (r == 0 && lane == 0) raise_error(a.err, ERR_ACCEPTED, q, (uint32_t)count);
       continue;
     }
+    if (count == 0) continue;  // (an idle request's ctx_len is not looked at)
     if (ctx < 1 || (int64_t)ctx - 1 + count > a.max_slots) {
       if (r == 0 && lane == 0) raise_error(a.err, ERR_CTX_LEN, q, (uint32_t)ctx);
       continue;

@@ -184,7 +184,7 @@ def test_append_refuses_bad_lengths_and_pages_on_the_device():
     cache = randn(g, bt.numel() + 3, b, 576)
     before = cache.clone()
     c, kr = randn(g, Q, rows, 512), randn(g, Q, rows, 64)
-    ctx, count = ints([0, 62, 1, 1, 1, 61]), ints([4, 4, 5, -1, 0, 4])
+    ctx, count = ints([0, 62, 1, 1, -7, 61]), ints([4, 4, 5, -1, 0, 4])
     isa.spin_latent_append(lt, rows, c, kr, cache, bt, ctx, count)
     changed = (cache != before).any(-1).nonzero()
     assert sorted(map(tuple, changed.tolist())) == sorted((int(bt[5, 3]), i) for i in range(12, 16))
@@ -276,6 +276,11 @@ ATTN = [
     (3, 2, 13, 100, [50, 333, 1], 16, F32, 512, 64),
     (4, 4, 3, 0, [1, 31, 33, 500], 32, F32, 64, 8),
     (2, 1, 9, 0, [100, 7], 64, BF16, 8, 128),
+    (140, 2, 16, 0, None, 64, BF16, 512, 64),
+    (300, 1, 3, 0, None, 16, F32, 64, 32),
+    (155, 1, 40, 700, None, 64, BF16, 512, 64),
+    (120, 1, 16, 2048, None, 64, BF16, 512, 64),
+    (60, 1, 16, 1500, None, 64, BF16, 512, 64),
 ]
 
 
@@ -478,11 +483,18 @@ PREFILL = [
     (3, 50, 2, [1, 100, 33], [50, 0, 20], 16, F32, 128, 32, 64, 32),
     (1, 90, 3, [200], None, 64, F32, 512, 64, 128, 128),
     (2, 9, 2, [5, 60], [9, 8], 64, F32, 8, 8, 8, 256),
+    (1, 700, 50, [900], None, 64, BF16, 512, 64, 128, 128),
+    (2, 520, 60, [600, 1], [520, 300], 64, BF16, 512, 64, 128, 128),
+    (300, 2, 1, None, None, 16, BF16, 512, 64, 128, 128),
+    (2, 30, 3, [4000, 3000], [30, 29], 64, BF16, 512, 64, 128, 128),
+    (1, 257, 2, [2500], None, 64, BF16, 512, 64, 128, 128),
 ]
 
 
 def prefill_case(Q, rows, H, ctxs, counts, b, dtype, dc, dr, dn, dv, **over):
     g = gen(Q * 100 + rows)
+    if ctxs is None:
+        ctxs = torch.randint(1, 300, (Q,), generator=torch.Generator().manual_seed(Q)).tolist()
     max_slots = max(c - 1 + rows for c in ctxs)
     ends = [c - 1 + n if n else 0 for c, n in zip(ctxs, counts or [rows] * Q)]
     over.setdefault("prefill_slots", sum(-(-e // 128) * 128 for e in ends))
@@ -581,10 +593,11 @@ def test_prefill_refuses_bad_lengths_pages_and_a_full_workspace(dtype):
     whole = lambda x, q: torch.equal(x[q], out[q])
     untouched = lambda x, q: bool((x[q] == 7).all())
     for c, n, word in ((ctx, ints([20, 21, 20, 5]), 4), (ctx, ints([20, -1, 20, 5]), 4),
-                       (ints([200, 0, 50, 1]), count, 1), (ints([200, 211, 50, 1]), count, 1)):
+                       (ints([200, 0, 50, 1]), count, 1), (ints([200, 211, 50, 1]), count, 1),
+                       (ints([200, 0, 50, 1]), ints([20, 0, 20, 5]), 0)):
         got = run_prefill(lt, 20, cache, bt, qv, w, c, n)
         assert untouched(got, 1) and all(whole(got, q) for q in (0, 2, 3))
-        assert isa.spin_latent_error(lt) == (6, word)
+        assert isa.spin_latent_error(lt) == (6 if word else 0, word)
     bt2 = bt.clone()
     bt2[1, 2] = -1              # slots 64..95 of request 1
     bt2[2, 3] = cache.shape[0]  # past request 2's slots: not looked at
