@@ -401,7 +401,8 @@ __device__ __forceinline__ int parts_of(int tail, int n) {
 struct AttMisc {
   uint64_t kfull[2], vfull[2];  // K(i), V(i) landed: barrier i % 2 (the ring holds less than two key tiles)
   uint64_t empty[kRing];
-  uint64_t qfull[2], sfull[2][2], pfull[2][2], odone[2];
+  uint64_t qfull[2], sfull[2], pfull[2][2], odone[2];
+  uint64_t turn[2];
   uint64_t done[2];
   int64_t tmp[33];
   uint32_t tmem;
@@ -482,10 +483,10 @@ __global__ void __launch_bounds__(kAttThreads, 1)
       mbar_init(bar(ms.vfull[t]), 1);
       mbar_init(bar(ms.done[t]), 1);
       mbar_init(bar(ms.qfull[t]), 128);
-      for (int half = 0; half < 2; ++half) {
-        mbar_init(bar(ms.sfull[t][half]), 1);
-        mbar_init(bar(ms.pfull[t][half]), 4);
-      }
+      mbar_init(bar(ms.sfull[t]), 1);
+      mbar_init(bar(ms.pfull[t][0]), 4);
+      mbar_init(bar(ms.pfull[t][1]), 4);
+      mbar_init(bar(ms.turn[t]), 1);
       mbar_init(bar(ms.odone[t]), 1);
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -538,28 +539,25 @@ __global__ void __launch_bounds__(kAttThreads, 1)
     // while one warp waits (75 cycles even where all is there) the other's
     // instructions run.
     const int t = warp - 9, nt = t ? n1 : n0;
-    const uint32_t id_s = idesc_bf16(128, 64, 0, 0);
+    const uint32_t id_s = idesc_bf16(128, 128, 0, 0);
     const uint32_t id_o = idesc_bf16(128, 128, 0, 1), id_o64 = idesc_bf16(128, 64, 0, 1);
     const uint32_t s_col = tmem + t * 128, o_col = tmem + kOCol + t * 128;
     const uint64_t ad = sw128_desc(q_at + t * kKBlocks * kBlk, 16, 1024);
     // The elected lane's parts, in loops of four instructions: the warp shares
-    // its instruction cache with the softmax.  S(j): 64 keys (half j % 2 of K at
-    // ring blocks s ..), columns b of K.
-    auto first = [&](int j, int b, int s) {
-      const uint32_t half = j & 1;
-      const uint64_t aq = ad + (uint64_t)b * (kBlk >> 4);
-      const uint64_t bd = sw128_desc(r_at + s * kBlk + half * (kBlk / 2), 16, 1024);
-      const uint32_t joined = b > 0, d = s_col + half * 64;
+    // its instruction cache with the softmax.  S(i): columns b of K, at ring block s.
+    auto first = [&](int b, int s) {
+      const uint64_t aq = ad + (uint64_t)b * (kBlk >> 4), bd = sw128_desc(r_at + s * kBlk, 16, 1024);
+      const uint32_t joined = b > 0;
 #pragma unroll
-      for (int kk = 0; kk < 4; ++kk) mma_f16(d, aq + 2 * kk, bd + 2 * kk, id_s, kk > 0 ? 1u : joined);
-      if (half) commit(bar(ms.empty[s]));
+      for (int kk = 0; kk < 4; ++kk) mma_f16(s_col, aq + 2 * kk, bd + 2 * kk, id_s, kk > 0 ? 1u : joined);
+      commit(bar(ms.empty[s]));
     };
-    // O += P(j) V(j), V at ring blocks s, s + 1.  V's two blocks are one operand 128 wide (with N = 64 an
-    // instruction takes as long), but where the ring ends between them.
-    auto second = [&](int j, int s) {
-      const uint32_t half = j & 1, p = s_col + half * 64, joined = j > 0;
+    // O += P V of half a key tile, V at ring blocks s, s + 1.  V's two blocks are one operand 128 wide (with N = 64
+    // an instruction takes as long), but where the ring ends between them.
+    auto second = [&](int half, int s, uint32_t joined) {
       const uint64_t bd = sw128_desc(r_at + s * kBlk + half * (kBlk / 2), kBlk, 1024);
       const uint64_t be = sw128_desc(r_at + half * (kBlk / 2), kBlk, 1024);
+      const uint32_t p = s_col + half * 64;
       if (s != kRing - 1) {
 #pragma unroll
         for (int k = 0; k < 4; ++k) mma_f16_ts(o_col, p + k * 8, bd + k * (2048 >> 4), id_o, k > 0 ? 1u : joined);
@@ -570,38 +568,50 @@ __global__ void __launch_bounds__(kAttThreads, 1)
           mma_f16_ts(o_col + 64, p + k * 8, be + k * (2048 >> 4), id_o64, k > 0 ? 1u : joined);
         }
       }
-      if (half) {
-        commit(bar(ms.empty[s]));
-        commit(bar(ms.empty[(s + 1) % kRing]));
-      }
       commit(bar(ms.odone[t]));
     };
     bool ok = true;
     if (nt) {
       ok = wait_warp(bar(ms.qfull[t]), 0, ctl);
-      // step j: the second product of half j, the first of half j + 2, whose place in TMEM half j leaves
-      for (int j = -2; ok && j < 2 * nt; ++j) {
-        if (j >= 0) {
-          const int i = j >> 1;
-          ok = ((j & 1) || wait_warp(bar(ms.vfull[i & 1]), (uint32_t)(i >> 1) & 1u, ctl)) &&
-               wait_warp(bar(ms.pfull[t][j & 1]), (uint32_t)i & 1u, ctl);
+      // Turn i: the second product of key tile i, the first of i + 1 (turn -1: the first alone).  The tiles take
+      // turns, so that one's softmax falls under the other's products (left to themselves they run in step).
+      for (int i = -1; ok && i < nt; ++i) {
+        if (i >= 0) {
+          const int s = (kKV * i + kKBlocks) % kRing;
+          ok = wait_warp(bar(ms.vfull[i & 1]), (uint32_t)(i >> 1) & 1u, ctl) &&
+               wait_warp(bar(ms.pfull[t][0]), (uint32_t)i & 1u, ctl);
+          if (ok && two && (t ? i < n0 : i > 0))
+            ok = wait_warp(bar(ms.turn[t]), (uint32_t)(t ? i : i - 1) & 1u, ctl);
+#pragma unroll 1
+          for (int half = 0; ok && half < 2; ++half) {
+            if (half) ok = wait_warp(bar(ms.pfull[t][1]), (uint32_t)i & 1u, ctl);
+            if (!ok) break;
+            fence_after();
+            if (elect()) second(half, s, half || i > 0 ? 1u : 0u);
+            __syncwarp();
+          }
           if (!ok) break;
-          fence_after();
-          if (elect()) second(j, (kKV * i + kKBlocks) % kRing);
+          if (elect()) {
+            commit(bar(ms.empty[s]));
+            commit(bar(ms.empty[(s + 1) % kRing]));
+          }
           __syncwarp();
         }
-        if (j + 2 < 2 * nt) {
-          const int i = (j + 2) >> 1;
-          ok = (j & 1) || wait_warp(bar(ms.kfull[i & 1]), (uint32_t)(i >> 1) & 1u, ctl);
+        if (i + 1 < nt) {
+          ok = wait_warp(bar(ms.kfull[(i + 1) & 1]), (uint32_t)((i + 1) >> 1) & 1u, ctl);
           if (!ok) break;
           fence_after();
 #pragma unroll 1
           for (int b = 0; b < kKBlocks; ++b) {
-            if (elect()) first(j + 2, b, (kKV * i + b) % kRing);
+            // (the turn goes on before its last instructions)
+            if (b == kKBlocks - 1 && two && i >= 0 && lane == 0) mbar_arrive(bar(ms.turn[t ^ 1]));
+            if (elect()) first(b, (kKV * (i + 1) + b) % kRing);
             __syncwarp();
           }
-          if (elect()) commit(bar(ms.sfull[t][j & 1]));
+          if (elect()) commit(bar(ms.sfull[t]));
           __syncwarp();
+        } else if (two && lane == 0) {
+          mbar_arrive(bar(ms.turn[t ^ 1]));
         }
       }
     }
@@ -661,10 +671,11 @@ __global__ void __launch_bounds__(kAttThreads, 1)
     const float scale = a.scale_log2;
     float m = -INFINITY, l = 0.f;
     bool ok = true;
+    // halves of 64 keys
     for (int j = 0; j < 2 * nt; ++j) {
       const uint32_t at = s_at + (j & 1) * 64;
-      // (S of half j follows the second product of half j - 2)
-      ok = wait_warp(bar(ms.sfull[t][j & 1]), (uint32_t)(j >> 1) & 1u, ctl);
+      // (S of a key tile follows the second products of the tile before)
+      if (!(j & 1)) ok = wait_warp(bar(ms.sfull[t]), (uint32_t)(j >> 1) & 1u, ctl);
       if (!ok) break;
       fence_after();
       uint32_t s[2][32];
@@ -690,7 +701,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
         m = mn;
         l *= f;
         if (j > 0) {
-          // (the second product of half j - 2 is complete, S of half j follows it)
+          // (of the second products only the last can still be running: S, or the half before, waited for the others)
           ok = wait_warp(bar(ms.odone[t]), (uint32_t)(j - 1) & 1u, ctl);
           if (!ok) break;
           fence_after();
@@ -709,12 +720,18 @@ __global__ void __launch_bounds__(kAttThreads, 1)
       float sum[4] = {0.f, 0.f, 0.f, 0.f};
       uint32_t p[32];
 #pragma unroll
-      for (int c = 0; c < 32; ++c) {
-        const int x = 2 * c;
-        const float p0 = ex2(fmaf(__uint_as_float(s[x >> 5][x & 31]), scale, -ref));
-        const float p1 = ex2(fmaf(__uint_as_float(s[x >> 5][(x & 31) + 1]), scale, -ref));
-        sum[c & 3] += p0 + p1;
-        p[c] = pack_bf16(p0, p1);
+      for (int c = 0; c < 32; c += 2) {
+        // four weights: two packed multiply-adds, two packed sums
+        float x[4];
+#pragma unroll
+        for (int k = 0; k < 4; k += 2) {
+          const int e = 2 * c + k;
+          fma2(x[k], x[k + 1], __uint_as_float(s[e >> 5][e & 31]), __uint_as_float(s[e >> 5][(e & 31) + 1]), scale, -ref);
+          x[k] = ex2(x[k]);
+          x[k + 1] = ex2(x[k + 1]);
+          add2(sum[k], sum[k + 1], x[k], x[k + 1]);
+          p[c + k / 2] = pack_bf16(x[k], x[k + 1]);
+        }
       }
       tmem_st32(at, p);
       tmem_wait_st();
