@@ -465,7 +465,7 @@ typedef enum { SPIN_ROPE_PLAIN = 0, SPIN_ROPE_LINEAR = 1, SPIN_ROPE_YARN = 2 } s
 
 typedef struct {
   int32_t num_requests;   /* Q: request slots */
-  int32_t max_slots;      /* KV capacity per request (slots) */
+  int32_t max_slots;      /* KV capacity per request (slots), at most 2^30 */
   int32_t block_size;     /* b: tokens per page, a power of two in 16..256 */
   int32_t num_heads;      /* attention heads, 1..256 */
   int32_t latent_dim;     /* width of c: a multiple of 8 in 8..512 */

@@ -239,8 +239,11 @@ __global__ void __launch_bounds__(kExpThreads, 1)
     // A slot tile's latents: a thread's slot into its TMEM lane, two elements a
     // column.  Slots past the request's last become zeros, and so do their keys
     // and values: a weight of 0 must meet no NaN.  The rotary part goes
-    // straight to the workspace.
-    auto load = [&](const ExpWalk& w) {
+    // straight to the workspace.  Returns whether the slot's latent holds what
+    // is not finite: its values are then written as zeros, so that rows before
+    // the slot, whose weights for it are 0, stay clean; rows that attend to it
+    // see the keys made of it.
+    auto load = [&](const ExpWalk& w) -> bool {
       const int slot = w.tile * kSlotTile + row;
       const uint4* src = nullptr;
       if (slot < w.end) {
@@ -251,6 +254,7 @@ __global__ void __launch_bounds__(kExpThreads, 1)
         else
           raise_error(a.err, ERR_PAGE, w.q, (uint32_t)page);
       }
+      __nv_bfloat162 zero = __floats2bfloat162_rn(0.f, 0.f), probe = zero;  // sum of 0 x: 0 or NaN
 #pragma unroll 1
       for (int c = 0; c < kDC / 64; ++c) {
         uint32_t v[32];
@@ -263,6 +267,12 @@ __global__ void __launch_bounds__(kExpThreads, 1)
           v[4 * k + 3] = x.w;
         }
         tmem_st32(tmem + lanes + kACol + (uint32_t)c * 32, v);
+#pragma unroll
+        for (int k = 0; k < 32; ++k) {
+          __nv_bfloat162 x;
+          memcpy(&x, &v[k], 4);
+          probe = __hfma2(x, zero, probe);
+        }
       }
       tmem_wait_st();
       fence_before();
@@ -273,19 +283,21 @@ __global__ void __launch_bounds__(kExpThreads, 1)
 #pragma unroll
         for (int c = 0; c < kDR / 8; ++c) dst[c] = src ? src[kDC / 8 + c] : make_uint4(0, 0, 0, 0);
       }
+      return !(__low2float(probe) == 0.f && __high2float(probe) == 0.f);
     };
     const bool store = (threadIdx.x & 127) == 0;  // the half's thread that issues its stores
-    if (half) load(w);
+    bool clear = half && load(w);
     int buf = 0;
     for (int i = 0; i < n_units; ++i) {
       const bool ok = wait_warp(bar(ms.dfull[half]), (uint32_t)i & 1u, ctl);
       if (bar_or(1 + half, 128, !ok)) break;  // (the warps leave together: they meet at barriers below)
       fence_after();
+      bool clear_next = clear;
       if (half && i + 1 < n_units) {
         // every product of this tile is complete: the next tile's latents first, so that its products begin
         ExpWalk next = w;
         next.step(a);
-        if (next.tile != w.tile || next.q != w.q) load(next);
+        if (next.tile != w.tile || next.q != w.q) clear_next = load(next);
       }
 #pragma unroll 1
       for (int c = 0; c < kHalf / 64; ++c) {
@@ -308,7 +320,7 @@ __global__ void __launch_bounds__(kExpThreads, 1)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const int x = 8 * j + 2 * e;
-            p[e] = pack_bf16(__uint_as_float(v[x >> 5][x & 31]), __uint_as_float(v[x >> 5][(x & 31) + 1]));
+            p[e] = clear ? 0u : pack_bf16(__uint_as_float(v[x >> 5][x & 31]), __uint_as_float(v[x >> 5][(x & 31) + 1]));
           }
           asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + ((j ^ (row & 7)) << 4)), "r"(p[0]),
                        "r"(p[1]), "r"(p[2]), "r"(p[3])
@@ -325,6 +337,7 @@ __global__ void __launch_bounds__(kExpThreads, 1)
         }
         buf ^= 1;
       }
+      clear = clear_next;
       w.step(a);
     }
     if (store) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");

@@ -57,7 +57,8 @@ bool eights(int x, int hi) { return x >= 8 && x <= hi && x % 8 == 0; }
 
 bool valid_config(const spin_latent_config* c) {
   if (!c) return false;
-  if (c->num_requests < 1 || c->num_requests > 16383 || c->max_slots < 1) return false;  // Q * rows fits a grid's y
+  if (c->num_requests < 1 || c->num_requests > 16383) return false;  // Q * rows fits a grid's y
+  if (c->max_slots < 1 || c->max_slots > (1 << 30)) return false;  // a tile past the last slot still fits 31 bits
   const int b = c->block_size;
   if (b < 16 || b > 256 || (b & (b - 1))) return false;
   if (c->num_heads < 1 || c->num_heads > 256) return false;
@@ -242,7 +243,7 @@ spin_status spin_rope(spin_latent lt, int64_t tokens, int heads, int head_dim, i
   const spin_latent_config& c = lt->cfg;
   if (tokens < 0 || heads < 1 || head_dim < c.rope_dim || offset < 0 || offset > head_dim - c.rope_dim)
     return SPIN_EINVAL;
-  if ((int64_t)heads * head_dim >= (int64_t(1) << 31)) return SPIN_EINVAL;
+  if ((int64_t)heads * head_dim > (int64_t(1) << 30)) return SPIN_EINVAL;  // 32-bit element counts, and a step on
   if (x_token_stride < 0 || x_head_stride < 0 || out_token_stride < 0 || out_head_stride < 0) return SPIN_EINVAL;
   if (tokens == 0) return SPIN_OK;
   if (!x || !out || !positions_dev) return SPIN_EINVAL;
@@ -374,6 +375,9 @@ spin_status spin_latent_prefill(spin_latent lt, int rows, const void* cache, int
       !cache_ok(lt, cache, num_pages, block_table, bt_stride))
     return SPIN_EINVAL;
   if (!c.prefill_slots) return SPIN_EUNSUPPORTED;
+  // blocks of the launch: 256 rows of a head each
+  if (rows > (1 << 30) || ((int64_t)rows + 255) / 256 * c.num_requests * c.num_heads >= (int64_t(1) << 31) - kTcBlocks)
+    return SPIN_EUNSUPPORTED;
   DeviceGuard guard(lt->device);
   if (guard.e != cudaSuccess) return cuda_status(guard.e);
   PrefillArgs a{};

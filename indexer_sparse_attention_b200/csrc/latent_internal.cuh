@@ -82,8 +82,8 @@ cudaError_t launch_append(const AppendArgs& a, int bf16, cudaStream_t s);
 // Absorbed attention: flat schedule.  An item is one (request, row); its
 // tokens are cut into tiles, at least one per item.  All items' tiles in a
 // row are the units; of the blocks that serve one group of heads (`ranges` of
-// them, or as many as there are units) block u takes units [U u / ranges, U (u + 1) / ranges), so ragged contexts
-// and few rows fill the SMs alike.  An item that lies in one block's range is
+// them, or as many as there are units) block u takes units [U u / ranges, U
+// (u + 1) / ranges), so ragged contexts and few rows fill the SMs alike.  An item that lies in one block's range is
 // finished there.  Else each block leaves its share -- maximum, sum and
 // unnormalised output, in fp32 -- in one of its two slots of the workspace
 // (slot 0: the item that holds the block's first unit, slot 1: the item that

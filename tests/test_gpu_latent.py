@@ -585,6 +585,26 @@ def test_prefill_takes_strided_and_unaligned_queries_and_graphs():
     del graph
 
 
+@pytest.mark.parametrize("value", [math.nan, math.inf, -math.inf])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_prefill_rows_before_a_token_that_is_not_finite_stay_clean(dtype, value):
+    """Slots 150 and 260 of the first request, of a chunk at slots 99..298:
+    their rows and those behind are NaN, the rows before and the other request
+    have the bits that they had.  All latents of a head's keys meet an
+    infinity as inf or -inf, so a logit sums both signs."""
+    lt, cache, bt, qv, w, ctx, count = prefill_case(2, 200, 2, [100, 40], [200, 130], 64, dtype, 512, 64, 128, 128)
+    out = run_prefill(lt, 200, cache, bt, qv, w, ctx, count)
+    for slot, where in ((150, slice(0, 512)), (260, slice(0, 512)), (150, slice(512, 576)), (198, slice(17, 18))):
+        broken = cache.clone()
+        kv = ref.slots_of(cache, bt, 0, ints([slot]).long()).to(dtype)
+        kv[:, where] = value
+        put(broken, bt, 0, ints([slot]).long(), kv)
+        got = run_prefill(lt, 200, broken, bt, qv, w, ctx, count)
+        row = slot - 99
+        assert torch.equal(got[0, :row], out[0, :row]) and torch.equal(got[1], out[1])
+        assert torch.isnan(got[0, row:]).all()
+
+
 @pytest.mark.parametrize("dtype", [BF16, F32])
 def test_prefill_refuses_bad_lengths_pages_and_a_full_workspace(dtype):
     lt, cache, bt, qv, w, ctx, count = prefill_case(4, 20, 2, [200, 100, 50, 1], [20, 10, 20, 5], 32, dtype, 512, 64,
@@ -609,6 +629,17 @@ def test_prefill_refuses_bad_lengths_pages_and_a_full_workspace(dtype):
     got = run_prefill(small, 20, cache, bt, qv, w, ctx, count)
     assert whole(got, 0) and whole(got, 1) and untouched(got, 2) and untouched(got, 3)
     assert isa.spin_latent_error(small) == (6, 16)
+
+
+def test_sizes_beyond_the_counters_are_refused():
+    lt, cache, bt, qv, w, ctx, count = prefill_case(1, 8, 2, [5], None, 64, BF16, 512, 64, 128, 128)
+    lib, p, s = isa.load(), cache.data_ptr(), torch.cuda.current_stream().cuda_stream
+    for rows in (2**30 + 1, 2**31 - 1):
+        assert lib.spin_latent_prefill(lt.handle, rows, p, cache.shape[0], bt.data_ptr(), bt.shape[1], p, 0, 0, p,
+                                       ctx.data_ptr(), None, p, s) == 7
+    for heads, width in ((2**20 + 1, 1024), (1, 2**30 + 8), (2**31 - 1, 64)):
+        assert lib.spin_rope(lt.handle, 1, heads, width, 0, p, 0, width, bt.data_ptr(), p, 0, width, s) == 1
+    assert isa.spin_latent_error(lt) == (0, 0)
 
 
 # ---------------------------------------------------------------------------

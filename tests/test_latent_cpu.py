@@ -49,7 +49,8 @@ def test_bytes_match_the_documented_parts(lib, over):
     {"rope_scaling": 3}, {"rope_base": 1.0}, {"rope_base": float("inf")},
     {"rope_scaling": 1, "rope_factor": 0.5}, {"rope_scaling": 2, "rope_original": 0},
     {"rope_scaling": 2, "beta_fast": 1.0}, {"rope_scaling": 2, "beta_slow": 0.0},
-    {"rope_scaling": 2, "attn_factor": -1.0}, {"max_slots": 2**31 - 1, "num_requests": 16383}])
+    {"rope_scaling": 2, "attn_factor": -1.0}, {"max_slots": 2**31 - 1, "num_requests": 16383},
+    {"max_slots": 2**30 + 1, "num_requests": 1}])
 def test_invalid_configs_are_refused(lib, over):
     c = _cfg(**over)
     assert isa.spin_latent_bytes(c) == 0
