@@ -415,6 +415,7 @@ struct AttMisc {
   uint64_t kfull[2], vfull[2];  // K(i), V(i) landed: barrier i % 2 (the ring holds less than two key tiles)
   uint64_t empty[kRing];
   uint64_t qfull[2], sfull[2], pfull[2][2], odone[2];
+  uint64_t olast[2];             // every second product of the row tile
   uint64_t turn[2];
   uint64_t done[2];
   int64_t tmp[33];
@@ -501,6 +502,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
       mbar_init(bar(ms.pfull[t][1]), 4);
       mbar_init(bar(ms.turn[t]), 1);
       mbar_init(bar(ms.odone[t]), 1);
+      mbar_init(bar(ms.olast[t]), 1);
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -607,6 +609,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
           if (elect()) {
             commit(bar(ms.empty[s]));
             commit(bar(ms.empty[(s + 1) % kRing]));
+            if (i == nt - 1) commit(bar(ms.olast[t]));
           }
           __syncwarp();
         }
@@ -753,8 +756,9 @@ __global__ void __launch_bounds__(kAttThreads, 1)
       if (lane == 0) mbar_arrive(bar(ms.pfull[t][j & 1]));
       l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
     }
-    // the last two second products, in order (parities tell only neighbours apart)
-    if (ok && nt) ok = wait_warp(bar(ms.odone[t]), 0, ctl) && wait_warp(bar(ms.odone[t]), 1, ctl);
+    // (a barrier of one phase: the products behind this warp's last weights may be complete before it looks, and
+    // odone's parity would not tell)
+    if (ok && nt) ok = wait_warp(bar(ms.olast[t]), 0, ctl);
     if (ok && w.parts > 1) {
       // a part: unnormalised, for the join
       const int64_t at = (int64_t)w.slot * 2 * kRowTile + t * kRowTile + tid;
