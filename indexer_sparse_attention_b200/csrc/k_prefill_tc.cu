@@ -15,8 +15,8 @@
 //               maximum, sum and rescaling need no exchange; the softmax
 //               reference moves only where a row's maximum has grown by more
 //               than 8 (log2 units), and then its warp rescales O.  K and V come
-//               as 16 KB blocks of 64 columns through one ring of eight, in the
-//               order of use.
+//               in 16 KB blocks (K: 64 columns of the 128 keys, V: 64 keys)
+//               through one ring of eight, in the order of use.
 #include <algorithm>
 
 #include "latent_internal.cuh"
@@ -426,8 +426,8 @@ constexpr uint32_t kAttSmem = 1024 + 2 * kKBlocks * kBlk + kRing * kBlk + sizeof
 static_assert(kAttSmem <= 227 * 1024, "one block's shared memory");
 
 __global__ void __launch_bounds__(kAttThreads, 1)
-    k_prefill_tc(const __grid_constant__ PrefillArgs a, const __grid_constant__ CUtensorMap map_kv,
-                 const __grid_constant__ CUtensorMap map_kr) {
+    k_prefill_tc(const __grid_constant__ PrefillArgs a, const __grid_constant__ CUtensorMap map_k,
+                 const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_kr) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* q_sm = smem;
@@ -529,10 +529,15 @@ __global__ void __launch_bounds__(kAttThreads, 1)
         if (lane == 0) {
           if (b == 0) mbar_expect_tx(kf, kKBlocks * kBlk);
           if (b == kKBlocks) mbar_expect_tx(vf, kVBlocks * kBlk);
-          if (b == 2)
+          if (b < 2) {
+            tma_load_2d(r_at + s * kBlk, &map_k, kf, b * 64, (int)(h * a.cap) + row);
+          } else if (b == 2) {
             tma_load_2d(r_at + s * kBlk, &map_kr, kf, 0, row);
-          else
-            tma_load_2d(r_at + s * kBlk, &map_kv, b < 2 ? kf : vf, (b < 2 ? b : b - 1) * 64, (int)(h * a.cap) + row);
+          } else {
+            const int y = (int)(h * a.cap) + row + (b - kKBlocks) * 64;
+            tma_load_2d(r_at + s * kBlk, &map_v, vf, kDN, y);
+            tma_load_2d(r_at + s * kBlk + kBlk / 2, &map_v, vf, kDN + 64, y);
+          }
         }
         if (b == 0) armed[i & 1] = par;
         if (b == kKBlocks) armed[2 + (i & 1)] = par;
@@ -555,7 +560,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
     // instructions run.
     const int t = warp - 9, nt = t ? n1 : n0;
     const uint32_t id_s = idesc_bf16(128, 128, 0, 0);
-    const uint32_t id_o = idesc_bf16(128, 128, 0, 1), id_o64 = idesc_bf16(128, 64, 0, 1);
+    const uint32_t id_o = idesc_bf16(128, 128, 0, 1);
     const uint32_t s_col = tmem + t * 128, o_col = tmem + kOCol + t * 128;
     const uint64_t ad = sw128_desc(q_at + t * kKBlocks * kBlk, 16, 1024);
     // The elected lane's parts, in loops of four instructions: the warp shares
@@ -567,22 +572,13 @@ __global__ void __launch_bounds__(kAttThreads, 1)
       for (int kk = 0; kk < 4; ++kk) mma_f16(s_col, aq + 2 * kk, bd + 2 * kk, id_s, kk > 0 ? 1u : joined);
       commit(bar(ms.empty[s]));
     };
-    // O += P V of half a key tile, V at ring blocks s, s + 1.  V's two blocks are one operand 128 wide (with N = 64
-    // an instruction takes as long), but where the ring ends between them.
+    // O += P V of half a key tile, V at ring block s.
     auto second = [&](int half, int s, uint32_t joined) {
-      const uint64_t bd = sw128_desc(r_at + s * kBlk + half * (kBlk / 2), kBlk, 1024);
-      const uint64_t be = sw128_desc(r_at + half * (kBlk / 2), kBlk, 1024);
+      const uint64_t bd = sw128_desc(r_at + s * kBlk, kBlk / 2, 1024);
       const uint32_t p = s_col + half * 64;
-      if (s != kRing - 1) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) mma_f16_ts(o_col, p + k * 8, bd + k * (2048 >> 4), id_o, k > 0 ? 1u : joined);
-      } else {
-#pragma unroll 1
-        for (int k = 0; k < 4; ++k) {
-          mma_f16_ts(o_col, p + k * 8, bd + k * (2048 >> 4), id_o64, k > 0 ? 1u : joined);
-          mma_f16_ts(o_col + 64, p + k * 8, be + k * (2048 >> 4), id_o64, k > 0 ? 1u : joined);
-        }
-      }
+      for (int k = 0; k < 4; ++k) mma_f16_ts(o_col, p + k * 8, bd + k * (2048 >> 4), id_o, k > 0 ? 1u : joined);
+      commit(bar(ms.empty[s]));
       commit(bar(ms.odone[t]));
     };
     bool ok = true;
@@ -592,7 +588,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
       // turns, so that one's softmax falls under the other's products (left to themselves they run in step).
       for (int i = -1; ok && i < nt; ++i) {
         if (i >= 0) {
-          const int s = (kKV * i + kKBlocks) % kRing;
+          const int s = kKV * i + kKBlocks;
           ok = wait_warp(bar(ms.vfull[i & 1]), (uint32_t)(i >> 1) & 1u, ctl) &&
                wait_warp(bar(ms.pfull[t][0]), (uint32_t)i & 1u, ctl);
           if (ok && two && (t ? i < n0 : i > 0))
@@ -602,15 +598,11 @@ __global__ void __launch_bounds__(kAttThreads, 1)
             if (half) ok = wait_warp(bar(ms.pfull[t][1]), (uint32_t)i & 1u, ctl);
             if (!ok) break;
             fence_after();
-            if (elect()) second(half, s, half || i > 0 ? 1u : 0u);
+            if (elect()) second(half, (s + half) % kRing, half || i > 0 ? 1u : 0u);
             __syncwarp();
           }
           if (!ok) break;
-          if (elect()) {
-            commit(bar(ms.empty[s]));
-            commit(bar(ms.empty[(s + 1) % kRing]));
-            if (i == nt - 1) commit(bar(ms.olast[t]));
-          }
+          if (i == nt - 1 && elect()) commit(bar(ms.olast[t]));
           __syncwarp();
         }
         if (i + 1 < nt) {
@@ -882,9 +874,10 @@ cudaError_t prepare_prefill_tc() {
 }
 
 cudaError_t launch_prefill_tc(const PrefillArgs& a, void* encode_fn, int sms, cudaStream_t s) {
-  CUtensorMap mw, mkv, mkr;
+  CUtensorMap mw, mkv, mv, mkr;
   if (!encode_rows(encode_fn, &mw, a.w, (uint64_t)a.H * kN, kDC, kDC * 2, kHalf) ||
       !encode_rows(encode_fn, &mkv, a.kv, (uint64_t)a.H * a.cap, kN, kN * 2, kRowTile) ||
+      !encode_rows(encode_fn, &mv, a.kv, (uint64_t)a.H * a.cap, kN, kN * 2, kRowTile / 2) ||
       !encode_rows(encode_fn, &mkr, a.kr, (uint64_t)a.cap, kDR, kDR * 2, kRowTile))
     return cudaErrorInvalidValue;
   cudaError_t e;
@@ -898,7 +891,7 @@ cudaError_t launch_prefill_tc(const PrefillArgs& a, void* encode_fn, int sms, cu
   b.planned = classes <= kPlanClasses;
   {
     PdlLaunch l(dim3((unsigned)(classes * a.H + (b.planned ? kTail : 0))), dim3(kAttThreads), kAttSmem, s);
-    e = cudaLaunchKernelEx(&l.cfg, k_prefill_tc, b, mkv, mkr);
+    e = cudaLaunchKernelEx(&l.cfg, k_prefill_tc, b, mkv, mv, mkr);
   }
   if (e != cudaSuccess || !b.planned) return e;
   PdlLaunch l(dim3((unsigned)std::min<int64_t>(kTail - 1, classes * a.H), kJoinGroups), dim3(256), 0, s);
