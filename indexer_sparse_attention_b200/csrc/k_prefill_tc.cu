@@ -243,36 +243,60 @@ __global__ void __launch_bounds__(kExpThreads, 1)
     // is not finite: its values are then written as zeros, so that rows before
     // the slot, whose weights for it are 0, stay clean; rows that attend to it
     // see the keys made of it.
+    // A thread reads its slot's 1152 bytes by itself, 128 at a time and one
+    // step ahead; the lines are asked into L2 all at once before (for the next
+    // tile while this one's products run).
+    auto place = [&](const ExpWalk& w, bool report) -> const uint4* {
+      const int slot = w.tile * kSlotTile + row;
+      if (slot >= w.end) return nullptr;
+      const int page = C.bt[(int64_t)w.q * C.bt_stride + (slot >> C.log2b)];
+      if (page < 0 || page >= C.num_pages) {
+        if (report) raise_error(a.err, ERR_PAGE, w.q, (uint32_t)page);
+        return nullptr;
+      }
+      return reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(C.data) +
+                                            (((int64_t)page << C.log2b) + (slot & (C.b - 1))) * (kDC + kDR));
+    };
+    auto ask = [&](const uint4* src) {
+      if (!src) return;
+#pragma unroll
+      for (int c = 0; c < (kDC + kDR) / 64; ++c)
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(src + 8 * c) : "memory");
+    };
     auto load = [&](const ExpWalk& w) -> bool {
       const int slot = w.tile * kSlotTile + row;
-      const uint4* src = nullptr;
-      if (slot < w.end) {
-        const int page = C.bt[(int64_t)w.q * C.bt_stride + (slot >> C.log2b)];
-        if (page >= 0 && page < C.num_pages)
-          src = reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(C.data) +
-                                               (((int64_t)page << C.log2b) + (slot & (C.b - 1))) * (kDC + kDR));
-        else
-          raise_error(a.err, ERR_PAGE, w.q, (uint32_t)page);
-      }
+      const uint4* src = place(w, true);
+      ask(src);
       __nv_bfloat162 zero = __floats2bfloat162_rn(0.f, 0.f), probe = zero;  // sum of 0 x: 0 or NaN
-#pragma unroll 1
-      for (int c = 0; c < kDC / 64; ++c) {
+      uint4 x[2][8];
+      auto fetch = [&](int c, uint4 (&x)[8]) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) x[k] = src ? src[8 * c + k] : make_uint4(0, 0, 0, 0);
+      };
+      auto keep = [&](int c, const uint4 (&x)[8]) {
         uint32_t v[32];
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-          const uint4 x = src ? src[8 * c + k] : make_uint4(0, 0, 0, 0);
-          v[4 * k] = x.x;
-          v[4 * k + 1] = x.y;
-          v[4 * k + 2] = x.z;
-          v[4 * k + 3] = x.w;
+          v[4 * k] = x[k].x;
+          v[4 * k + 1] = x[k].y;
+          v[4 * k + 2] = x[k].z;
+          v[4 * k + 3] = x[k].w;
         }
         tmem_st32(tmem + lanes + kACol + (uint32_t)c * 32, v);
 #pragma unroll
         for (int k = 0; k < 32; ++k) {
-          __nv_bfloat162 x;
-          memcpy(&x, &v[k], 4);
-          probe = __hfma2(x, zero, probe);
+          __nv_bfloat162 e;
+          memcpy(&e, &v[k], 4);
+          probe = __hfma2(e, zero, probe);
         }
+      };
+      fetch(0, x[0]);
+#pragma unroll 1
+      for (int c = 0; c < kDC / 64; c += 2) {
+        fetch(c + 1, x[1]);
+        keep(c, x[0]);
+        if (c + 2 < kDC / 64) fetch(c + 2, x[0]);
+        keep(c + 1, x[1]);
       }
       tmem_wait_st();
       fence_before();
@@ -286,7 +310,14 @@ __global__ void __launch_bounds__(kExpThreads, 1)
       return !(__low2float(probe) == 0.f && __high2float(probe) == 0.f);
     };
     const bool store = (threadIdx.x & 127) == 0;  // the half's thread that issues its stores
+    auto ask_behind = [&](ExpWalk at, int unit) {  // the tile behind that of `at`, the block's unit `unit`
+      if (unit + a.H - at.h >= n_units) return;
+      at.h = a.H - 1;
+      at.step(a);
+      ask(place(at, false));
+    };
     bool clear = half && load(w);
+    if (half) ask_behind(w, 0);
     int buf = 0;
     for (int i = 0; i < n_units; ++i) {
       const bool ok = wait_warp(bar(ms.dfull[half]), (uint32_t)i & 1u, ctl);
@@ -297,7 +328,10 @@ __global__ void __launch_bounds__(kExpThreads, 1)
         // every product of this tile is complete: the next tile's latents first, so that its products begin
         ExpWalk next = w;
         next.step(a);
-        if (next.tile != w.tile || next.q != w.q) clear_next = load(next);
+        if (next.tile != w.tile || next.q != w.q) {
+          clear_next = load(next);
+          ask_behind(next, i + 1);
+        }
       }
 #pragma unroll 1
       for (int c = 0; c < kHalf / 64; ++c) {
@@ -363,7 +397,7 @@ constexpr int kKBlocks = 3, kVBlocks = 2, kKV = kKBlocks + kVBlocks;
 // keys into as many parts as fill the round, each part's maximum, sum and
 // unnormalised output left in the workspace for the join (a chunk of few rows
 // on a long context is cut into up to kMaxParts).
-constexpr int kTail = 148, kMaxParts = 16, kPlanClasses = 256, kMinPart = 4;
+constexpr int kTail = 148, kMaxParts = 16, kPlanClasses = 256, kMinPart = 8;
 struct Plan {
   int order[kPlanClasses];  // classes by rank; the empty ones last
   int tiles[kPlanClasses];  // key tiles by class
@@ -438,7 +472,10 @@ __global__ void __launch_bounds__(kAttThreads, 1)
   const Ctl ctl{&ms.abort_flag, a.err};
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-  pdl_enter();
+  // What does not depend on the expanded keys runs while those are made: the
+  // expansion has begun, so the lengths and the block table are there.  (A
+  // block with nothing to do waits for it all the same: the launch must not
+  // complete before it.)
   Unit w;
   if (a.planned) {
     Plan& p = *reinterpret_cast<Plan*>(r_sm);  // (the ring is not in use yet)
@@ -446,15 +483,15 @@ __global__ void __launch_bounds__(kAttThreads, 1)
     const int units = p.used * a.H, tail = tail_of(a, p), whole = units - tail;
     int u = blockIdx.x;
     if (u >= whole) {
-      if (!tail) return;
+      if (!tail) return pdl_enter();
       const int most = min(kTail / tail, kMaxParts), x = u - whole;
       u = whole + x / most;
-      if (u >= units) return;
+      if (u >= units) return pdl_enter();
       w = unit_at(a, p, u);
       w.part = x % most;
       w.parts = parts_of(tail, p.tiles[p.order[a.Q == 1 ? u % p.used : u / a.H]]);
       w.slot = x;
-      if (w.part >= w.parts) return;
+      if (w.part >= w.parts) return pdl_enter();
     } else {
       w = unit_at(a, p, u);
     }
@@ -467,9 +504,9 @@ __global__ void __launch_bounds__(kAttThreads, 1)
   }
   const int h = w.h, q = w.q, r0 = w.r0;
   const Chunk ch = prefill_chunk(a, q, false);
-  if (r0 >= ch.count) return;
+  if (r0 >= ch.count) return pdl_enter();
   const int64_t off = prefill_rows_before(a, q, ms.tmp);
-  if (off + ch.end > a.cap) return;
+  if (off + ch.end > a.cap) return pdl_enter();
   {
     const LatentCache& C = a.cache;
     int bad = 0;
@@ -477,7 +514,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
       const int page = C.bt[(int64_t)q * C.bt_stride + i];
       bad |= page < 0 || page >= C.num_pages;
     }
-    if (__syncthreads_or(bad)) return;
+    if (__syncthreads_or(bad)) return pdl_enter();
   }
   // rows and key tiles of the two row tiles
   const int rows0 = min(ch.count - r0, kRowTile), rows1 = max(0, min(ch.count - r0 - kRowTile, kRowTile));
@@ -512,6 +549,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
   fence_after();
   const uint32_t tmem = ms.tmem;
   constexpr uint32_t kOCol = 256;
+  pdl_enter();
 
   if (warp == 8) {
     // ======================= copies =======================
@@ -888,7 +926,7 @@ cudaError_t launch_prefill_tc(const PrefillArgs& a, void* encode_fn, int sms, cu
   if (e != cudaSuccess) return e;
   const int64_t classes = (int64_t)a.Q * ((a.rows + 2 * kRowTile - 1) / (2 * kRowTile));
   PrefillArgs b = a;
-  b.planned = classes <= kPlanClasses;
+  b.planned = classes <= kPlanClasses && (a.max_slots + kRowTile - 1) / kRowTile >= 2 * kMinPart;
   {
     PdlLaunch l(dim3((unsigned)(classes * a.H + (b.planned ? kTail : 0))), dim3(kAttThreads), kAttSmem, s);
     e = cudaLaunchKernelEx(&l.cfg, k_prefill_tc, b, mkv, mv, mkr);
