@@ -448,7 +448,8 @@ SPIN_API int64_t spin_mask_stride(spin_state st);
  * p_r = ctx_len[q] - 1 + r and sees slots 0..p_r; a position is a slot index.
  * The conventions at the top of this file hold: asynchronous, no allocation,
  * argument errors in the return value, device-side errors in the handle's own
- * device error word (spin_latent_error), deterministic results. */
+ * device error word (spin_latent_error), deterministic results.  Outputs do not
+ * overlap inputs (spin_rope says where they may). */
 typedef enum {
   SPIN_ROPE_INTERLEAVED = 0, /* element pairs (2 i, 2 i + 1) */
   SPIN_ROPE_HALF = 1         /* element pairs (i, i + rope_dim / 2) */
@@ -492,9 +493,9 @@ typedef struct {
 
 typedef struct spin_latent_s* spin_latent;
 
-/* Bytes of device memory a handle needs: the error word, the partial sums of
- * a context that several thread blocks share, and for prefill_slots > 0 the
- * expanded keys and values (prefill_slots * (num_heads * (nope_dim + v_dim) +
+/* Bytes of device memory a handle needs: the error word, the rotary
+ * frequencies, the partial sums of a context that several thread blocks share,
+ * and for prefill_slots > 0 the expanded keys and values (prefill_slots * (num_heads * (nope_dim + v_dim) +
  * rope_dim) elements).  Returns 0 for an invalid config. */
 SPIN_API size_t spin_latent_bytes(const spin_latent_config* cfg);
 
@@ -513,9 +514,9 @@ SPIN_API spin_status spin_latent_destroy(spin_latent lt);
  * strides between tokens and between heads (the head itself is contiguous).
  * positions_dev [tokens] int32, of either sign: -p undoes p (a rotation's
  * transpose), up to attn_factor.  out == x with x's strides rotates in
- * place; any other overlap is not allowed.  Angles are exact to 2^-31 of a
- * turn at every position: the turn's fraction is an integer product modulo
- * 2^64. */
+ * place; any other overlap is not allowed.  heads * head_dim is at most 2^30.
+ * Angles are exact to 2^-31 of a turn at every position: the turn's fraction is
+ * an integer product modulo 2^64. */
 SPIN_API spin_status spin_rope(spin_latent lt, int64_t tokens, int heads, int head_dim, int offset, const void* x,
                                int64_t x_token_stride, int64_t x_head_stride, const int32_t* positions_dev,
                                void* out, int64_t out_token_stride, int64_t out_head_stride, spin_stream_t stream);
@@ -527,8 +528,8 @@ SPIN_API spin_status spin_rope(spin_latent lt, int64_t tokens, int heads, int he
  * stay as they are.  block_table [Q][bt_stride] as for the indexer.  A
  * request with ctx_len < 1, a row_count outside 0..rows or a last slot past
  * max_slots sets ERR_CTX_LEN (bit 0) or ERR_ACCEPTED (bit 2) and writes
- * nothing (with row_count 0 its ctx_len is not looked at); a page outside the cache sets ERR_PAGE (bit 1) and that token is
- * not written.  Two rows that share a slot of one page leave either's entry. */
+ * nothing (with row_count 0 its ctx_len is not looked at); a page outside the
+ * cache sets ERR_PAGE (bit 1) and that token is not written.  Two rows that share a slot of one page leave either's entry. */
 SPIN_API spin_status spin_latent_append(spin_latent lt, int rows, const void* c_dev, int64_t c_token_stride,
                                         const void* kr_dev, int64_t kr_token_stride, void* cache, int32_t num_pages,
                                         const int32_t* block_table, int32_t bt_stride, const int32_t* ctx_len_dev,
@@ -567,7 +568,9 @@ SPIN_API spin_status spin_latent_attention(spin_latent lt, int rows, const void*
  * out of range sets ERR_CTX_LEN or ERR_ACCEPTED, one that no longer fits
  * prefill_slots (in request order) ERR_CAPACITY (bit 4), one with a page
  * outside the cache among those of its slots ERR_PAGE; its rows stay
- * unwritten.  Slots past a request's last row never reach the result. */
+ * unwritten.  Slots that a row does not see never reach its result, whatever
+ * latents they hold.  SPIN_EUNSUPPORTED without prefill_slots, or where
+ * num_requests * num_heads * ceil(rows / 256) is near 2^31 or more. */
 SPIN_API spin_status spin_latent_prefill(spin_latent lt, int rows, const void* cache, int32_t num_pages,
                                          const int32_t* block_table, int32_t bt_stride, const void* q,
                                          int64_t q_token_stride, int64_t q_head_stride, const void* w_kv,

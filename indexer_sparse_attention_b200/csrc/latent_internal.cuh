@@ -283,7 +283,7 @@ __device__ __forceinline__ Chunk prefill_chunk(const PrefillArgs& a, int q, bool
   if (c.count < 0 || c.count > a.rows) {
     if (report) raise_error(a.err, ERR_ACCEPTED, q, (uint32_t)c.count);
     c.count = 0;
-  } else if (c.count && (c.ctx < 1 || (int64_t)c.ctx - 1 + c.count > a.max_slots)) {  // (idle: ctx_len is not looked at)
+  } else if (c.count && (c.ctx < 1 || (int64_t)c.ctx - 1 + c.count > a.max_slots)) {
     if (report) raise_error(a.err, ERR_CTX_LEN, q, (uint32_t)c.ctx);
     c.count = 0;
   }

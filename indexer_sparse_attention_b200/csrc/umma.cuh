@@ -99,7 +99,8 @@ __device__ __forceinline__ bool wait_warp2(uint32_t bar0, uint32_t parity0, uint
 __device__ __forceinline__ bool wait_warp3(uint32_t bar0, uint32_t parity0, uint32_t bar1, uint32_t parity1,
                                            uint32_t bar2, uint32_t parity2, Ctl c) {
   const int i = threadIdx.x & 3;
-  return __all_sync(0xffffffffu, wait(i == 0 ? bar0 : i == 1 ? bar1 : bar2, i == 0 ? parity0 : i == 1 ? parity1 : parity2, c));
+  const uint32_t bar = i == 0 ? bar0 : i == 1 ? bar1 : bar2, parity = i == 0 ? parity0 : i == 1 ? parity1 : parity2;
+  return __all_sync(0xffffffffu, wait(bar, parity, c));
 }
 // One lane of a converged warp.  tcgen05.mma and its descriptors live on the
 // uniform datapath: issued by the elected lane of a warp whose control flow
@@ -146,16 +147,6 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map
       "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(
           dst),
       "l"((uint64_t)map), "r"(bar), "r"(x), "r"(y)
-      : "memory");
-}
-// Four rows of a map whose boxes are one row high; a row outside the matrix
-// reads as zeros.
-__device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y0, int y1,
-                                            int y2, int y3) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes [%0], "
-      "[%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(dst),
-      "l"((uint64_t)map), "r"(bar), "r"(x), "r"(y0), "r"(y1), "r"(y2), "r"(y3)
       : "memory");
 }
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }

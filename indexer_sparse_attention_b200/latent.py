@@ -243,7 +243,8 @@ def spin_latent_append(lt: SpinLatent, rows: int, c: torch.Tensor, k_rope: torch
     cp, ct, _ = _tokens(lt, c, "c", (lt.requests, rows, lt.latent))
     kp, kt, _ = _tokens(lt, k_rope, "k_rope", (lt.requests, rows, lt.rope))
     _call("spin_latent_append", lt.handle, rows, cp, ct, kp, kt, *_cache(lt, cache, block_table),
-          _dense(lt, ctx_len, "ctx_len", torch.int32, lt.per_request), _dense(lt, row_count, "row_count", torch.int32, lt.per_request),
+          _dense(lt, ctx_len, "ctx_len", torch.int32, lt.per_request),
+          _dense(lt, row_count, "row_count", torch.int32, lt.per_request),
           _stream(lt, stream))
 
 
@@ -277,7 +278,8 @@ def spin_latent_prefill(lt: SpinLatent, rows: int, cache: torch.Tensor, block_ta
     qp = _tokens(lt, q, "q", (Q, rows, H, cfg.nope_dim + cfg.rope_dim))
     _call("spin_latent_prefill", lt.handle, rows, *_cache(lt, cache, block_table), *qp,
           _dense(lt, w_kv, "w_kv", lt.dtype, (H, cfg.nope_dim + cfg.v_dim, cfg.latent_dim)),
-          _dense(lt, ctx_len, "ctx_len", torch.int32, lt.per_request), _dense(lt, row_count, "row_count", torch.int32, lt.per_request),
+          _dense(lt, ctx_len, "ctx_len", torch.int32, lt.per_request),
+          _dense(lt, row_count, "row_count", torch.int32, lt.per_request),
           _dense(lt, out, "out", lt.dtype, (Q, rows, H, cfg.v_dim)), _stream(lt, stream))
 
 
