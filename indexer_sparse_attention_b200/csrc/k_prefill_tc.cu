@@ -263,9 +263,11 @@ __global__ void __launch_bounds__(kExpThreads, 1)
     // is not finite: its values are then written as zeros, so that rows before
     // the slot, whose weights for it are 0, stay clean; rows that attend to it
     // see the keys made of it.
-    // A thread reads its slot's 1152 bytes by itself, 128 at a time and one
+    // A warp brings its 32 slots' rows by way of shared memory (the output
+    // buffers' place), eight lanes a 128-byte line, 64 columns at a time and one
     // step ahead; the lines are asked into L2 all at once before (for the next
-    // tile while this one's products run).
+    // tile while this one's products run).  Each thread reading its own slot's
+    // row took 10 us a tile, five units' time.
     auto place = [&](const ExpWalk& w, bool report) -> const uint4* {
       const int slot = w.tile * kSlotTile + row;
       if (slot >= w.end) return nullptr;
@@ -287,21 +289,42 @@ __global__ void __launch_bounds__(kExpThreads, 1)
       const int slot = w.tile * kSlotTile + row;
       const uint4* src = place(w, true);
       ask(src);
-      __nv_bfloat162 zero = __floats2bfloat162_rn(0.f, 0.f), probe = zero;  // sum of 0 x: 0 or NaN
-      uint4 x[2][8];
-      auto fetch = [&](int c, uint4 (&x)[8]) {
+      // this lane's piece of rows lane / 8 + 4 j
+      const char* from[8];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) x[k] = src ? src[8 * c + k] : make_uint4(0, 0, 0, 0);
+      for (int j = 0; j < 8; ++j)
+        from[j] = reinterpret_cast<const char*>(__shfl_sync(0xffffffffu, (unsigned long long)src, (lane >> 3) + 4 * j));
+      const uint32_t stage = o_at + (half * kOutBufs) * kBlk + (warp & 3) * 4096;
+      auto fetch = [&](int c) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int to = (lane >> 3) + 4 * j;
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                           stage + (c & 1) * kBlk + to * 128 + (((lane & 7) ^ (to & 7)) << 4)),
+                       "l"(from[j] ? from[j] + c * 128 + (lane & 7) * 16 : reinterpret_cast<const char*>(C.data)),
+                       "r"(from[j] ? 16u : 0u)
+                       : "memory");
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
       };
-      auto keep = [&](int c, const uint4 (&x)[8]) {
+      __nv_bfloat162 zero = __floats2bfloat162_rn(0.f, 0.f), probe = zero;  // sum of 0 x: 0 or NaN
+      fetch(0);
+#pragma unroll 1
+      for (int c = 0; c < kDC / 64; ++c) {
+        if (c + 1 < kDC / 64) {
+          fetch(c + 1);
+          asm volatile("cp.async.wait_group 1;" ::: "memory");
+        } else {
+          asm volatile("cp.async.wait_group 0;" ::: "memory");
+        }
+        __syncwarp();
         uint32_t v[32];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          v[4 * k] = x[k].x;
-          v[4 * k + 1] = x[k].y;
-          v[4 * k + 2] = x[k].z;
-          v[4 * k + 3] = x[k].w;
-        }
+        for (int k = 0; k < 8; ++k)
+          asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                       : "=r"(v[4 * k]), "=r"(v[4 * k + 1]), "=r"(v[4 * k + 2]), "=r"(v[4 * k + 3])
+                       : "r"(stage + (c & 1) * kBlk + lane * 128 + ((k ^ (lane & 7)) << 4))
+                       : "memory");
         tmem_st32(tmem + lanes + kACol + (uint32_t)c * 32, v);
 #pragma unroll
         for (int k = 0; k < 32; ++k) {
@@ -309,23 +332,18 @@ __global__ void __launch_bounds__(kExpThreads, 1)
           memcpy(&e, &v[k], 4);
           probe = __hfma2(e, zero, probe);
         }
-      };
-      fetch(0, x[0]);
-#pragma unroll 1
-      for (int c = 0; c < kDC / 64; c += 2) {
-        fetch(c + 1, x[1]);
-        keep(c, x[0]);
-        if (c + 2 < kDC / 64) fetch(c + 2, x[0]);
-        keep(c + 1, x[1]);
+        __syncwarp();  // the buffer has been read
       }
       tmem_wait_st();
       fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(ms.afull));
       if (w.h == 0) {  // (a tile that another block begins has its rotary part from there)
-        uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(a.kr) + (w.off + slot) * kDR);
+        char* dst = reinterpret_cast<char*>(a.kr) + (w.off + slot - lane + (lane >> 3)) * (kDR * 2) + (lane & 7) * 16;
 #pragma unroll
-        for (int c = 0; c < kDR / 8; ++c) dst[c] = src ? src[kDC / 8 + c] : make_uint4(0, 0, 0, 0);
+        for (int j = 0; j < 8; ++j)
+          *reinterpret_cast<uint4*>(dst + j * (4 * kDR * 2)) =
+              from[j] ? *reinterpret_cast<const uint4*>(from[j] + kDC * 2 + (lane & 7) * 16) : make_uint4(0, 0, 0, 0);
       }
       return !(__low2float(probe) == 0.f && __high2float(probe) == 0.f);
     };
@@ -349,6 +367,8 @@ __global__ void __launch_bounds__(kExpThreads, 1)
         ExpWalk next = w;
         next.step(a);
         if (next.tile != w.tile || next.q != w.q) {
+          if (store) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // (the loads pass through their place)
+          bar_sync(1 + half, 128);
           clear_next = load(next);
           ask_behind(next, i + 1);
         }
