@@ -54,7 +54,7 @@ constexpr float kLazy = 8.0f;
 // ---------------------------------------------------------------------------
 // expansion
 // ---------------------------------------------------------------------------
-// warps 0..3 the keys' epilogue, 4..7 latents and the values' epilogue, 8 copies, 9 MMA issue
+// warps 0..3 half of the latents' columns and the keys' epilogue, 4..7 the other half and the values', 8 copies, 9 MMA issue
 constexpr int kExpThreads = 320;
 constexpr int kHalf = kN / 2;        // a unit's product is taken in two halves, the keys and the values
 constexpr int kStageK = 128;         // reduction width of a stage of weights
@@ -69,11 +69,19 @@ struct ExpMisc {
   uint64_t dfull[2], dfree[2];       // accumulators
   uint64_t done;
   int tmp[35];
+  uint8_t odd[2][kRowTile];          // the first half of a latent's columns is not all finite; by turns of tiles
   uint32_t tmem;
   int abort_flag;
 };
 constexpr uint32_t kExpSmem = 1024 + kBStages * kBBytes + 2 * kOutBufs * kBlk + sizeof(ExpMisc);
 static_assert(kExpSmem <= 227 * 1024, "one block's shared memory");
+
+// Slot tiles of a request, and one more than the workspace holds at most (so
+// that sums over 320 requests fit 31 bits).
+__device__ __forceinline__ int slot_tiles(const PrefillArgs& a, int q, bool report) {
+  if (q >= a.Q) return 0;
+  return min((prefill_chunk(a, q, report).end + kSlotTile - 1) / kSlotTile, (int)(a.cap / kSlotTile) + 1);
+}
 
 // The walk over units (slot tile, head), heads within a tile.
 struct ExpWalk {
@@ -112,7 +120,7 @@ __global__ void __launch_bounds__(kExpThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     ms.abort_flag = 0;
-    mbar_init(bar(ms.afull), 4);
+    mbar_init(bar(ms.afull), 8);
     for (int i = 0; i < kBStages; ++i) {
       mbar_init(bar(ms.bfull[i]), 1);
       mbar_init(bar(ms.bfree[i]), 1);
@@ -136,42 +144,58 @@ __global__ void __launch_bounds__(kExpThreads, 1)
   ExpWalk w{};
   int n_units = 0;
   {
-    int total = 0, tiles_before = 0;  // units; all fit 31 bits (the host's check)
-    int carry = 0;
-    for (int base = 0; base < a.Q; base += kExpThreads) {
-      const int q = base + (int)threadIdx.x;
-      const int t = q < a.Q ? (prefill_chunk(a, q, blockIdx.x == 0).end + kSlotTile - 1) / kSlotTile : 0;
-      int sum;
-      const int ex = carry + block_exclusive_scan(t, ms.tmp, &sum);
-      const bool fits = (int64_t)(ex + t) * kSlotTile <= a.cap;
-      if (q < a.Q && t && !fits && blockIdx.x == 0) raise_error(a.err, ERR_CAPACITY, q, (uint32_t)t * kSlotTile);
-      int kept;
-      block_exclusive_scan(fits ? t : 0, ms.tmp, &kept);
-      total += kept;
-      carry += sum;
-    }
-    total *= a.H;
-    const int u0 = range_begin(total, gridDim.x, blockIdx.x), u1 = range_begin(total, gridDim.x, blockIdx.x + 1);
-    n_units = u1 - u0;
-    // the request that holds unit u0
-    const int want = u0 / a.H;
-    carry = 0;
-    for (int base = 0; base < a.Q && n_units; base += kExpThreads) {
-      const int q = base + (int)threadIdx.x;
-      const int t = q < a.Q ? (prefill_chunk(a, q, false).end + kSlotTile - 1) / kSlotTile : 0;
-      int sum;
-      const int ex = carry + block_exclusive_scan(t, ms.tmp, &sum);
-      if (ex <= want && want < ex + t) {
-        ms.tmp[33] = q;
-        ms.tmp[34] = ex;
+    const bool report = blockIdx.x == 0 && (a.Q > 32 || warp == 0);
+    const auto full = [&](int q, int t) { raise_error(a.err, ERR_CAPACITY, q, (uint32_t)t * kSlotTile); };
+    const int cap_tiles = (int)(a.cap / kSlotTile);
+    int u0 = 0;
+    auto share = [&](int tiles) {  // the block's units; all fit 31 bits (the host's check)
+      u0 = range_begin(tiles * a.H, gridDim.x, blockIdx.x);
+      n_units = range_begin(tiles * a.H, gridDim.x, blockIdx.x + 1) - u0;
+      return u0 / a.H;
+    };
+    int tiles_before = 0, want;
+    if (a.Q <= 32) {
+      // each warp by itself, a request a lane: no barriers
+      const int t = slot_tiles(a, lane, report), upto = warp_inclusive_scan(t);
+      if (report && t && upto > cap_tiles) full(lane, t);
+      const uint32_t fits = __ballot_sync(0xffffffffu, upto <= cap_tiles);
+      const int total = __shfl_sync(0xffffffffu, upto, fits ? 31 - __clz((int)fits) : 0);
+      want = share(fits ? total : 0);
+      const uint32_t here = __ballot_sync(0xffffffffu, upto - t <= want && want < upto);
+      w.q = here ? __ffs((int)here) - 1 : 0;
+      tiles_before = __shfl_sync(0xffffffffu, upto - t, w.q);
+    } else {
+      constexpr int kMany = 1 << 30;  // more tiles than any workspace has
+      int total = 0, carry = 0;
+      for (int base = 0; base < a.Q; base += kExpThreads) {
+        const int q = base + (int)threadIdx.x, t = slot_tiles(a, q, report);
+        int sum, kept;
+        const int upto = carry + block_exclusive_scan(t, ms.tmp, &sum) + t;
+        if (report && t && upto > cap_tiles) full(q, t);
+        block_exclusive_scan(upto <= cap_tiles ? t : 0, ms.tmp, &kept);
+        total += kept;
+        carry = min(carry + sum, kMany);
       }
-      carry += sum;
-      if (carry > want) break;
+      want = share(total);
+      carry = 0;
+      for (int base = 0; base < a.Q && n_units; base += kExpThreads) {
+        const int q = base + (int)threadIdx.x, t = slot_tiles(a, q, false);
+        int sum;
+        const int ex = carry + block_exclusive_scan(t, ms.tmp, &sum);
+        if (ex <= want && want < ex + t) {
+          ms.tmp[33] = q;
+          ms.tmp[34] = ex;
+        }
+        carry = min(carry + sum, kMany);
+        if (carry > want) break;
+      }
+      __syncthreads();
+      if (n_units) {
+        w.q = ms.tmp[33];
+        tiles_before = ms.tmp[34];
+      }
     }
-    __syncthreads();
     if (n_units) {
-      w.q = ms.tmp[33];
-      tiles_before = ms.tmp[34];
       w.off = (int64_t)tiles_before * kSlotTile;
       w.tile = want - tiles_before;
       w.h = u0 - want * a.H;
@@ -259,11 +283,12 @@ __global__ void __launch_bounds__(kExpThreads, 1)
     // A slot tile's latents: a thread's slot into its TMEM lane, two elements a
     // column.  Slots past the request's last become zeros, and so do their keys
     // and values: a weight of 0 must meet no NaN.  The rotary part goes
-    // straight to the workspace.  Returns whether the slot's latent holds what
-    // is not finite: its values are then written as zeros, so that rows before
+    // straight to the workspace.  Returns whether this half of the slot's latent holds what
+    // is not finite: the slot's values are then written as zeros, so that rows before
     // the slot, whose weights for it are 0, stay clean; rows that attend to it
     // see the keys made of it.
-    // A warp brings its 32 slots' rows by way of shared memory (the output
+    // Each half of the warps takes four of the eight 64-column pieces.
+    // A warp brings its 32 slots' pieces by way of shared memory (the output
     // buffers' place), eight lanes a 128-byte line, 64 columns at a time and one
     // step ahead; the lines are asked into L2 all at once before (for the next
     // tile while this one's products run).  Each thread reading its own slot's
@@ -285,7 +310,7 @@ __global__ void __launch_bounds__(kExpThreads, 1)
       for (int c = 0; c < (kDC + kDR) / 64; ++c)
         asm volatile("prefetch.global.L2 [%0];" ::"l"(src + 8 * c) : "memory");
     };
-    auto load = [&](const ExpWalk& w) -> bool {
+    auto load = [&](const ExpWalk& w, int n) -> bool {  // n: the block's n-th tile
       const int slot = w.tile * kSlotTile + row;
       const uint4* src = place(w, true);
       ask(src);
@@ -308,10 +333,11 @@ __global__ void __launch_bounds__(kExpThreads, 1)
         asm volatile("cp.async.commit_group;" ::: "memory");
       };
       __nv_bfloat162 zero = __floats2bfloat162_rn(0.f, 0.f), probe = zero;  // sum of 0 x: 0 or NaN
-      fetch(0);
+      constexpr int kPieces = kDC / 64 / 2;
+      fetch(half * kPieces);
 #pragma unroll 1
-      for (int c = 0; c < kDC / 64; ++c) {
-        if (c + 1 < kDC / 64) {
+      for (int c = half * kPieces; c < (half + 1) * kPieces; ++c) {
+        if (c + 1 < (half + 1) * kPieces) {
           fetch(c + 1);
           asm volatile("cp.async.wait_group 1;" ::: "memory");
         } else {
@@ -334,18 +360,20 @@ __global__ void __launch_bounds__(kExpThreads, 1)
         }
         __syncwarp();  // the buffer has been read
       }
+      const bool odd = !(__low2float(probe) == 0.f && __high2float(probe) == 0.f);
+      if (!half) ms.odd[n & 1][row] = odd;
       tmem_wait_st();
       fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(ms.afull));
-      if (w.h == 0) {  // (a tile that another block begins has its rotary part from there)
+      if (half && w.h == 0) {  // (a tile that another block begins has its rotary part from there)
         char* dst = reinterpret_cast<char*>(a.kr) + (w.off + slot - lane + (lane >> 3)) * (kDR * 2) + (lane & 7) * 16;
 #pragma unroll
         for (int j = 0; j < 8; ++j)
           *reinterpret_cast<uint4*>(dst + j * (4 * kDR * 2)) =
               from[j] ? *reinterpret_cast<const uint4*>(from[j] + kDC * 2 + (lane & 7) * 16) : make_uint4(0, 0, 0, 0);
       }
-      return !(__low2float(probe) == 0.f && __high2float(probe) == 0.f);
+      return odd;
     };
     const bool store = (threadIdx.x & 127) == 0;  // the half's thread that issues its stores
     auto ask_behind = [&](ExpWalk at, int unit) {  // the tile behind that of `at`, the block's unit `unit`
@@ -354,24 +382,30 @@ __global__ void __launch_bounds__(kExpThreads, 1)
       at.step(a);
       ask(place(at, false));
     };
-    bool clear = half && load(w);
-    if (half) ask_behind(w, 0);
-    int buf = 0;
+    // the next tile's latents, once every product of this one is complete
+    auto reload = [&](const ExpWalk& next, int n) -> bool {
+      if (store) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // (they pass through the stores' place)
+      bar_sync(1 + half, 128);
+      return load(next, n);
+    };
+    int buf = 0, nload = 0;
+    bool mine = load(w, 0), ok = true;
+    bool clear = false;  // this slot's values are written as zeros
+    if (half) {
+      ask_behind(w, 0);
+      ok = wait_warp(bar(ms.afull), 0, ctl);
+      clear = mine || ms.odd[0][row];
+    }
     for (int i = 0; i < n_units; ++i) {
-      const bool ok = wait_warp(bar(ms.dfull[half]), (uint32_t)i & 1u, ctl);
+      ok = ok && wait_warp(bar(ms.dfull[half]), (uint32_t)i & 1u, ctl);
       if (bar_or(1 + half, 128, !ok)) break;  // (the warps leave together: they meet at barriers below)
       fence_after();
-      bool clear_next = clear;
-      if (half && i + 1 < n_units) {
-        // every product of this tile is complete: the next tile's latents first, so that its products begin
-        ExpWalk next = w;
-        next.step(a);
-        if (next.tile != w.tile || next.q != w.q) {
-          if (store) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // (the loads pass through their place)
-          bar_sync(1 + half, 128);
-          clear_next = load(next);
-          ask_behind(next, i + 1);
-        }
+      ExpWalk next = w;
+      if (i + 1 < n_units) next.step(a);
+      const bool turn = next.tile != w.tile || next.q != w.q;
+      if (half && turn) {  // before the epilogue, so that the next products begin
+        mine = reload(next, nload + 1);
+        ask_behind(next, i + 1);
       }
 #pragma unroll 1
       for (int c = 0; c < kHalf / 64; ++c) {
@@ -411,8 +445,18 @@ __global__ void __launch_bounds__(kExpThreads, 1)
         }
         buf ^= 1;
       }
-      clear = clear_next;
-      w.step(a);
+      if (turn) {
+        // (of the keys' warps the epilogue comes first: the values' products run meanwhile)
+        ++nload;
+        ok = half ? wait_warp(bar(ms.afull), (uint32_t)nload & 1u, ctl)
+                  : wait_warp(bar(ms.dfull[1]), (uint32_t)i & 1u, ctl);
+        if (bar_or(1 + half, 128, !ok)) break;
+        if (half)
+          clear = mine || ms.odd[nload & 1][row];
+        else
+          reload(next, nload);
+      }
+      w = next;
     }
     if (store) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   }
