@@ -110,12 +110,11 @@ static_assert(smem_bytes(kTcHeads) <= 227 * 1024, "one block's shared memory");
 struct Walk {
   int item, whole, later;  // later: the first item that is not whole
   int first, at, stop;
-  int q, r, end, n, t0, t1;
+  int q, r, n, t0, t1;
   __device__ __forceinline__ void open(const AttnArgs& a) {
     q = item / a.rows;
     r = item - q * a.rows;
-    end = attn_end(a, q, r);
-    n = attn_tiles(a, end);
+    n = attn_tiles(a, a.list ? 0 : attn_end(a, q, r));  // (lists: the length is not waited for)
     t0 = whole > 0 ? 0 : at - first;
     t1 = whole > 0 ? n : min(n, stop - first);
   }
@@ -209,7 +208,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const LatentCache& C = a.cache;
     const char* data = reinterpret_cast<const char*>(C.data);
     struct Look {
-      int item, q, end, flags;
+      int item, q, r, ctx, flags;
       int slot[2], page[2];
     };
     int tile = 0;
@@ -224,7 +223,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!more) continue;
         x[v].item = w.item;
         x[v].q = w.q;
-        x[v].end = w.end;
+        x[v].r = w.r;
+        x[v].ctx = __ldg(a.ctx_len + w.q);
         x[v].flags = k < w.t1 - 1 ? 0 : w.last() ? 6 : 2;
         const int e0 = k * kTok + 2 * lane;
 #pragma unroll
@@ -248,9 +248,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int v = 0; v < 2; ++v)  // their pages
         if (x[v].q >= 0) {
           const int32_t* bt = C.bt + (int64_t)x[v].q * C.bt_stride;
+          const int end = attn_end_at(a, x[v].ctx, x[v].r);
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            if (x[v].slot[i] >= x[v].end) x[v].slot[i] = -1;
+            if (x[v].slot[i] >= end) x[v].slot[i] = -1;
             x[v].page[i] = x[v].slot[i] >= 0 ? __ldg(bt + (x[v].slot[i] >> C.log2b)) : 0;
           }
         }
@@ -472,7 +473,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool run = true;
     while (run) {
       w.open(a);
-      if (w.end == 0 && w.t0 == 0 && threadIdx.x == 0) raise_error(a.err, ERR_CTX_LEN, w.q, (uint32_t)a.ctx_len[w.q]);
+      if (threadIdx.x == 0 && w.t0 == 0 && attn_end(a, w.q, w.r) == 0)
+        raise_error(a.err, ERR_CTX_LEN, w.q, (uint32_t)a.ctx_len[w.q]);
       float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
       int flags;
       bool alive = true;

@@ -330,6 +330,8 @@ spin_status spin_latent_attention(spin_latent lt, int rows, const void* cache, i
     a.ranges = (int)std::min<int64_t>(std::max(1, blocks / a.ngroups), (int64_t)a.Q * rows * ((n + tile - 1) / tile));
     a.whole = 0;
     a.rest = a.ranges;
+    a.per = (a.topk + tile - 1) / tile;
+    a.total = a.Q * rows * a.per;
   };
   cudaError_t e;
   if (attn_tc_supported(a, bf16)) {
@@ -341,7 +343,7 @@ spin_status spin_latent_attention(spin_latent lt, int rows, const void* cache, i
       //   or cut evenly, `cut` blocks each (the join costs about as much as 2 tiles),
       //   or as one run of units over all blocks (and blocks that change items, about 5 tiles),
       // whichever ends first.  128 items of 32 tiles on 148 blocks: 73 us as one run, 61 us a block each.
-      const int items = a.Q * rows, per = (a.topk + kTcTile - 1) / kTcTile;
+      const int items = a.Q * rows, per = a.per;
       a.whole = items / a.ranges;
       const int left = items - a.whole * a.ranges;
       if (left) {
@@ -353,6 +355,9 @@ spin_status spin_latent_attention(spin_latent lt, int rows, const void* cache, i
           a.ranges = left;
           a.whole = 1;
         }
+        a.total = (items - a.whole * a.ranges) * per;
+      } else {
+        a.total = 0;
       }
     }
     e = launch_attn_tc(a, (cudaStream_t)stream);

@@ -115,19 +115,21 @@ struct AttnArgs {
   int ranges;                // blocks per head group, at most
   int whole;                 // items that each block takes whole (lists only)
   int rest;                  // of the blocks, those that share the other items, at most
+  int per;                   // lists: tiles of an item, and of the items that are not taken whole
+  int total;
   float* part;               // [ngroups * ranges * 2][group][dc] unnormalised outputs
   float2* part_ml;           // [ngroups * ranges * 2][group] (maximum in log2 units, sum)
 };
 
 // The last slot + 1 that row r of request q may attend to (0: its ctx_len is
 // out of range), and the number of tiles of the item.
-__device__ __forceinline__ int attn_end(const AttnArgs& a, int q, int r) {
-  const int ctx = a.ctx_len[q];
+__device__ __forceinline__ int attn_end_at(const AttnArgs& a, int ctx, int r) {
   return (ctx >= 1 && (int64_t)ctx + a.rows - 1 <= a.max_slots) ? ctx + r : 0;
 }
+__device__ __forceinline__ int attn_end(const AttnArgs& a, int q, int r) { return attn_end_at(a, a.ctx_len[q], r); }
 __device__ __forceinline__ int attn_tiles(const AttnArgs& a, int end) {
-  const int n = a.list ? a.topk : end;
-  return n > 0 ? (n + a.tile - 1) / a.tile : 1;
+  if (a.list) return a.per;
+  return end > 0 ? (end + a.tile - 1) / a.tile : 1;
 }
 
 // First unit of range u of `ranges` over `total` >= ranges units, and the
@@ -159,12 +161,12 @@ __device__ __forceinline__ Place attn_place(const AttnArgs& a, int item, int u, 
   const int items = a.Q * a.rows;
   Place p;
   if (a.list) {
-    const int per = (a.topk + a.tile - 1) / a.tile, base = a.whole * a.ranges;
-    p.total = (items - base) * per;
-    p.ranges = min(a.rest, p.total);
-    const int i = item >= 0 ? item - base : u < p.ranges ? range_begin(p.total, p.ranges, u) / per : 0;
+    const int base = a.whole * a.ranges;
+    p.total = a.total;
+    p.ranges = min(a.rest, a.total);
+    const int i = item >= 0 ? item - base : u < p.ranges ? range_begin(p.total, p.ranges, u) / a.per : 0;
     p.item = base + i;
-    p.first = i * per;
+    p.first = i * a.per;
     return p;
   }
   // every item's tiles, one after the other
