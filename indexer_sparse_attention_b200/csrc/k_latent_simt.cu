@@ -25,7 +25,7 @@ constexpr float kNegInf = -INFINITY;
 struct Tile {
   float* q;     // [kNH][W]
   float* kv;    // [kT][stride]
-  float* p;     // [kNH][kT]
+  float* p;     // [kT][kNH]
   float* alpha; // [kNH]
   int W, stride, voff, dv;
 
@@ -36,11 +36,13 @@ struct Tile {
     const float* qh = q + h * W;
     const float* kj = kv + j * stride;
     float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
+#pragma unroll 4
     for (int i = 0; i < W; i += 4) {  // W is a multiple of 8
-      s0 = fmaf(qh[i], kj[i], s0);
-      s1 = fmaf(qh[i + 1], kj[i + 1], s1);
-      s2 = fmaf(qh[i + 2], kj[i + 2], s2);
-      s3 = fmaf(qh[i + 3], kj[i + 3], s3);
+      const float4 x = *reinterpret_cast<const float4*>(qh + i);
+      s0 = fmaf(x.x, kj[i], s0);
+      s1 = fmaf(x.y, kj[i + 1], s1);
+      s2 = fmaf(x.z, kj[i + 2], s2);
+      s3 = fmaf(x.w, kj[i + 3], s3);
     }
     const float s = seen ? ((s0 + s1) + (s2 + s3)) * scale : kNegInf;
     float mt = s;
@@ -55,7 +57,7 @@ struct Tile {
     for (int d = 16; d >= 1; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
     l = l * al + sum;
     m = mn;
-    p[h * kT + j] = e;
+    p[j * kNH + h] = e;
     if (j == 0) alpha[h] = al;
     __syncthreads();
 #pragma unroll
@@ -65,14 +67,15 @@ struct Tile {
 #pragma unroll
       for (int h2 = 0; h2 < kNH; ++h2) o[c][h2] *= alpha[h2];
       const float* v = kv + voff + d;
+#pragma unroll 4
       for (int t = 0; t < kT; ++t) {
         const float x = v[t * stride];
+        float w[kNH];
 #pragma unroll
-        for (int h2 = 0; h2 < kNH; ++h2) {
-          // a weight of exactly 0 takes nothing from the token, whatever it holds
-          const float w = p[h2 * kT + t];
-          o[c][h2] = w != 0.f ? fmaf(w, x, o[c][h2]) : o[c][h2];
-        }
+        for (int k = 0; k < kNH; k += 4) *reinterpret_cast<float4*>(w + k) = *reinterpret_cast<const float4*>(p + t * kNH + k);
+        // a weight of exactly 0 takes nothing from the token, whatever it holds
+#pragma unroll
+        for (int h2 = 0; h2 < kNH; ++h2) o[c][h2] = w[h2] != 0.f ? fmaf(w[h2], x, o[c][h2]) : o[c][h2];
       }
     }
     __syncthreads();
@@ -104,13 +107,12 @@ __global__ void __launch_bounds__(kThreads) k_attn_simt(const __grid_constant__ 
     const int n = attn_tiles(a, end);
     const int t0 = at - first, t1 = min(n, stop - first);
     __syncthreads();
-    for (int i = threadIdx.x; i < kNH * W; i += kThreads) {
-      const int h = h0 + i / W, d = i % W;
-      float v = 0.f;
-      if (h < a.H)
-        v = d < C.dc ? to_f32(reinterpret_cast<const T*>(a.ql)[item * a.ql_tok + h * a.ql_head + d])
-                     : to_f32(reinterpret_cast<const T*>(a.qr)[item * a.qr_tok + h * a.qr_head + d - C.dc]);
-      t.q[i] = v;
+    {
+      const int h = h0 + warp;
+      const T* ql = reinterpret_cast<const T*>(a.ql) + item * a.ql_tok + h * a.ql_head;
+      const T* qr = reinterpret_cast<const T*>(a.qr) + item * a.qr_tok + h * a.qr_head - C.dc;
+#pragma unroll 4
+      for (int d = lane; d < W; d += 32) t.q[warp * W + d] = h < a.H ? to_f32(d < C.dc ? ql[d] : qr[d]) : 0.f;
     }
     float m = kNegInf, l = 0.f, o[2][kNH] = {};
     for (int k = t0; k < t1; ++k) {
@@ -399,24 +401,24 @@ __global__ void __launch_bounds__(kThreads) k_prefill_simt(const __grid_constant
   const int64_t token0 = (int64_t)q * a.rows;
   for (int r0 = blockIdx.x * kNH; r0 < ch.count; r0 += gridDim.x * kNH) {
     __syncthreads();
-    for (int i = threadIdx.x; i < kNH * W; i += kThreads) {
-      const int r = r0 + i / W, d = i % W;
-      t.q[i] = r < ch.count ? to_f32(reinterpret_cast<const T*>(a.q)[(token0 + r) * a.q_tok + h * a.q_head + d]) : 0.f;
+    {
+      const T* x = reinterpret_cast<const T*>(a.q) + (token0 + r0 + warp) * a.q_tok + h * a.q_head;
+#pragma unroll 4
+      for (int d = lane; d < W; d += 32) t.q[warp * W + d] = r0 + warp < ch.count ? to_f32(x[d]) : 0.f;
     }
     const int pos = ch.ctx - 1 + r0 + warp;
     const int last = min(ch.ctx - 1 + r0 + kNH - 1, ch.end - 1);
     float m = kNegInf, l = 0.f, o[2][kNH] = {};
     for (int j0 = 0; j0 <= last; j0 += kT) {
       __syncthreads();
-      for (int i = threadIdx.x; i < kT * (W + a.dv); i += kThreads) {
-        const int j = i / (W + a.dv), d = i - j * (W + a.dv);
-        float v = 0.f;
-        if (j0 + j < ch.end) {
-          const int64_t s = off + j0 + j;
-          const T* kv = reinterpret_cast<const T*>(a.kv) + (h * a.cap + s) * N;
-          v = to_f32(d < a.dn ? kv[d] : d < W ? reinterpret_cast<const T*>(a.kr)[s * dr + d - a.dn] : kv[d - dr]);
-        }
-        t.kv[j * t.stride + d] = v;
+      for (int j = warp; j < kT; j += kThreads / 32) {
+        const int64_t s = off + j0 + j;
+        const bool live = j0 + j < ch.end;
+        const T* kv = reinterpret_cast<const T*>(a.kv) + (h * a.cap + s) * N;
+        const T* kr = reinterpret_cast<const T*>(a.kr) + s * dr - a.dn;
+#pragma unroll 4
+        for (int d = lane; d < W + a.dv; d += 32)
+          t.kv[j * t.stride + d] = live ? to_f32(d < a.dn ? kv[d] : d < W ? kr[d] : kv[d - dr]) : 0.f;
       }
       __syncthreads();
       t.step(m, l, o, a.scale_log2, j0 + lane <= pos && j0 + lane <= last);
