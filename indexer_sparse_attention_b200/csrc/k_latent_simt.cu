@@ -300,6 +300,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_attn_combine(const __grid_c
 // Expanded form
 // ---------------------------------------------------------------------------
 constexpr int kES = 32, kEK = 32;  // slots of a block, reduction step
+constexpr int kEStride = kES + 4;  // of a step's slots in shared memory: 16-byte aligned, spread over banks
 
 // kv[h][off + s] = W_h c_s for a tile of kES slots and one head; head 0 also
 // copies the shared key part.  grid (slot tiles, heads, requests).
@@ -318,8 +319,8 @@ __global__ void __launch_bounds__(kThreads) k_expand_simt(const __grid_constant_
     if (blockIdx.x == 0 && h == 0 && threadIdx.x == 0) raise_error(a.err, ERR_CAPACITY, q, (uint32_t)ch.end);
     return;
   }
-  float* cs = sm;                  // [kEK][kES + 1]
-  float* ws = sm + kEK * (kES + 1);  // [N][kEK + 1]
+  float* cs = sm;                    // [kEK][kEStride]
+  float* ws = sm + kEK * kEStride;  // [N][kEK + 1]
   for (int s0 = blockIdx.x * kES; s0 < ch.end; s0 += gridDim.x * kES) {
     __syncthreads();
     if (threadIdx.x < kES) {
@@ -331,7 +332,7 @@ __global__ void __launch_bounds__(kThreads) k_expand_simt(const __grid_constant_
     for (int k0 = 0; k0 < C.dc; k0 += kEK) {
       for (int i = threadIdx.x; i < kES * kEK; i += kThreads) {
         const int s = i / kEK, k = i % kEK;
-        cs[k * (kES + 1) + s] = (row[s] >= 0 && k0 + k < C.dc)
+        cs[k * kEStride + s] = (row[s] >= 0 && k0 + k < C.dc)
                                     ? to_f32(reinterpret_cast<const T*>(C.data)[row[s] * W + k0 + k]) : 0.f;
       }
       for (int i = threadIdx.x; i < N * kEK; i += kThreads) {
@@ -347,7 +348,13 @@ __global__ void __launch_bounds__(kThreads) k_expand_simt(const __grid_constant_
           for (int k = 0; k < kEK; ++k) {
             const float w = ws[n * (kEK + 1) + k];
 #pragma unroll
-            for (int s = 0; s < kES; ++s) acc[c][s] = fmaf(w, cs[k * (kES + 1) + s], acc[c][s]);
+            for (int s = 0; s < kES; s += 4) {
+              const float4 x = *reinterpret_cast<const float4*>(cs + k * kEStride + s);
+              acc[c][s] = fmaf(w, x.x, acc[c][s]);
+              acc[c][s + 1] = fmaf(w, x.y, acc[c][s + 1]);
+              acc[c][s + 2] = fmaf(w, x.z, acc[c][s + 2]);
+              acc[c][s + 3] = fmaf(w, x.w, acc[c][s + 3]);
+            }
           }
       }
       __syncthreads();
@@ -411,14 +418,24 @@ __global__ void __launch_bounds__(kThreads) k_prefill_simt(const __grid_constant
     float m = kNegInf, l = 0.f, o[2][kNH] = {};
     for (int j0 = 0; j0 <= last; j0 += kT) {
       __syncthreads();
-      for (int j = warp; j < kT; j += kThreads / 32) {
-        const int64_t s = off + j0 + j;
-        const bool live = j0 + j < ch.end;
-        const T* kv = reinterpret_cast<const T*>(a.kv) + (h * a.cap + s) * N;
-        const T* kr = reinterpret_cast<const T*>(a.kr) + s * dr - a.dn;
-#pragma unroll 4
-        for (int d = lane; d < W + a.dv; d += 32)
-          t.kv[j * t.stride + d] = live ? to_f32(d < a.dn ? kv[d] : d < W ? kr[d] : kv[d - dr]) : 0.f;
+      // 16 bytes a lane (all widths are multiples of 8), a warp's four slots at once
+      constexpr int V = 16 / (int)sizeof(T);
+      const T* kv = reinterpret_cast<const T*>(a.kv) + (h * a.cap + off + j0 + warp) * N;
+      const T* kr = reinterpret_cast<const T*>(a.kr) + (off + j0 + warp) * dr;
+      for (int d = lane * V; d < W + a.dv; d += 32 * V) {
+        const T* src = d < a.dn ? kv + d : d < W ? kr + (d - a.dn) : kv + (d - dr);
+        const int64_t step = 8 * (d < a.dn || d >= W ? N : dr);
+        uint4 x[kT / 8];
+#pragma unroll
+        for (int i = 0; i < kT / 8; ++i)
+          x[i] = j0 + warp + 8 * i < ch.end ? *reinterpret_cast<const uint4*>(src + i * step) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int i = 0; i < kT / 8; ++i) {
+          const T* e = reinterpret_cast<const T*>(&x[i]);
+          float* dst = t.kv + (warp + 8 * i) * t.stride + d;
+#pragma unroll
+          for (int k = 0; k < V; ++k) dst[k] = to_f32(e[k]);
+        }
       }
       __syncthreads();
       t.step(m, l, o, a.scale_log2, j0 + lane <= pos && j0 + lane <= last);
@@ -440,7 +457,7 @@ constexpr int kMaxSmem = 160 * 1024;
 size_t attn_smem(int W) {
   return sizeof(float) * (kNH * W + kT * (W + 1) + kNH * kT + kNH + 2) + sizeof(int64_t) * kT;
 }
-size_t expand_smem(int N) { return sizeof(float) * (kEK * (kES + 1) + (size_t)N * (kEK + 1)); }
+size_t expand_smem(int N) { return sizeof(float) * (kEK * kEStride + (size_t)N * (kEK + 1)); }
 size_t prefill_smem(int W, int dv) { return sizeof(float) * (kNH * W + kT * ((W + dv) | 1) + kNH * kT + kNH); }
 
 template <typename T>
