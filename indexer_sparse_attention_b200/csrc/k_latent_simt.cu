@@ -512,6 +512,9 @@ cudaError_t launch_prefill_simt(const PrefillArgs& a, int bf16, cudaStream_t s) 
   auto kernel = bf16 ? k_prefill_simt<__nv_bfloat16> : k_prefill_simt<float>;
   const int64_t tiles = ((int64_t)a.rows + kNH - 1) / kNH;
   PdlLaunch l(dim3((unsigned)(tiles < 4096 ? tiles : 4096), (unsigned)a.H, (unsigned)a.Q), dim3(kThreads), smem, s);
+  // Not scheduled beside the expansion: its blocks would gather on the SMs that have room early (126 us, not 87, for 3
+  // x 150 fp32 rows on 400 slots x 5 heads).
+  l.cfg.numAttrs = 0;
   return cudaLaunchKernelEx(&l.cfg, kernel, a);
 }
 
