@@ -488,6 +488,7 @@ PREFILL = [
     (300, 2, 1, None, None, 16, BF16, 512, 64, 128, 128),
     (2, 30, 3, [4000, 3000], [30, 29], 64, BF16, 512, 64, 128, 128),
     (1, 257, 2, [2500], None, 64, BF16, 512, 64, 128, 128),
+    (1, 130, 1, [40000], None, 128, BF16, 512, 64, 128, 128),  # blocks that change slot tiles with every unit
 ]
 
 
@@ -629,6 +630,34 @@ def test_prefill_refuses_bad_lengths_pages_and_a_full_workspace(dtype):
     got = run_prefill(small, 20, cache, bt, qv, w, ctx, count)
     assert whole(got, 0) and whole(got, 1) and untouched(got, 2) and untouched(got, 3)
     assert isa.spin_latent_error(small) == (6, 16)
+
+
+@pytest.mark.parametrize("Q,fit", [(30, 17), (40, 17), (400, 341)])
+def test_prefill_of_many_requests_in_a_workspace_for_some(Q, fit):
+    """Requests of two slot tiles each, in order: those behind the first that does not fit stay unwritten."""
+    lt, cache, bt, qv, w, ctx, count = prefill_case(Q, 5, 2, [150] * Q, None, 16, BF16, 512, 64, 128, 128)
+    out = run_prefill(lt, 5, cache, bt, qv, w, ctx, count)
+    check_prefill(lt, 5, cache, bt, qv, w, ctx, count, out)
+    assert isa.spin_latent_error(lt) == (0, 0)
+    small, *_ = prefill_case(Q, 5, 2, [150] * Q, None, 16, BF16, 512, 64, 128, 128, prefill_slots=256 * fit + 128)
+    got = run_prefill(small, 5, cache, bt, qv, w, ctx, count)
+    assert torch.equal(got[:fit], out[:fit]) and bool((got[fit:] == 7).all())
+    assert isa.spin_latent_error(small) == (6, 16)
+
+
+def test_a_token_that_is_not_finite_in_a_context_of_many_slot_tiles():
+    """One head, so that a block's units are slot tiles that follow one another, each with its own flags."""
+    lt, cache, bt, qv, w, ctx, count = prefill_case(1, 300, 1, [40000], None, 128, BF16, 512, 64, 128, 128)
+    out = run_prefill(lt, 300, cache, bt, qv, w, ctx, count)
+    for slot, where in ((40100, slice(0, 1)), (40100, slice(511, 512)), (40298, slice(0, 512))):
+        kv = ref.slots_of(cache, bt, 0, ints([slot]).long()).to(BF16)
+        kept = kv.clone()
+        kv[:, where] = math.nan
+        put(cache, bt, 0, ints([slot]).long(), kv)
+        got = run_prefill(lt, 300, cache, bt, qv, w, ctx, count)
+        put(cache, bt, 0, ints([slot]).long(), kept)
+        row = slot - 39999
+        assert torch.equal(got[0, :row], out[0, :row]) and torch.isnan(got[0, row:]).all()
 
 
 def test_sizes_beyond_the_counters_are_refused():
