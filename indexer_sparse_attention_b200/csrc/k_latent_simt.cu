@@ -6,8 +6,9 @@
 //   o' = o 2^(m - m') + sum 2^(s_j - m') v_j
 // in log2 units (the softmax scale carries log2 e), everything in fp32.
 // Bound by shared memory, which each multiply-add of a score reads twice: at 96
-// requests x 128 heads x 2048 slots 14.5 ms (3.8 TFLOP/s); at what it is for, one
-// fp32 request of 8 heads with 256 slots of 320, 14.9 us, most of that the start
+// requests x 128 heads x 2048 slots 14.5 ms (3.8 TFLOP/s; before queries and
+// weights were read four at a time); at what it is for, one
+// fp32 request of 8 heads with 256 slots of 320, 13 us, most of that the start
 // and the join.
 #include "latent_internal.cuh"
 
@@ -72,7 +73,8 @@ struct Tile {
         const float x = v[t * stride];
         float w[kNH];
 #pragma unroll
-        for (int k = 0; k < kNH; k += 4) *reinterpret_cast<float4*>(w + k) = *reinterpret_cast<const float4*>(p + t * kNH + k);
+        for (int k = 0; k < kNH; k += 4)
+          *reinterpret_cast<float4*>(w + k) = *reinterpret_cast<const float4*>(p + t * kNH + k);
         // a weight of exactly 0 takes nothing from the token, whatever it holds
 #pragma unroll
         for (int h2 = 0; h2 < kNH; ++h2) o[c][h2] = w[h2] != 0.f ? fmaf(w[h2], x, o[c][h2]) : o[c][h2];

@@ -5,9 +5,10 @@
 //               matrix product M = slots, N = 128 twice, K = 512.  A block keeps
 //               the latents of 128 slots in TMEM and streams the heads' weights,
 //               160 KB in flight, so L2 -> SM carries 256 KB a unit (slot tile,
-//               head) instead of 384.  Bound by that stream, then by the products
-//               (4160 cycles a unit): 107 us for 16K slots x 32 heads, 1.28
-//               PFLOP/s, where a large plain product reaches 1.65.
+//               head) instead of 384.  105 us for 16K slots x 32 heads, 1.30
+//               PFLOP/s, where a large plain product reaches 1.65: a unit
+//               takes 4780 cycles, its products alone 4160, bringing in a slot
+//               tile 6000.
 // k_prefill_tc  causal attention of 256 rows of one head: two 128-row tiles take
 //               turns on the tensor cores, one's softmax under the other's
 //               products:
@@ -25,7 +26,7 @@
 //               memory a cycle in S (all there is), together with the chain S ->
 //               weights -> second product -> S of each row tile: P takes the place
 //               of its S, and TMEM has no room for another.  Without the softmax
-//               the call would take 0.98 ms instead of 1.07.
+//               the call took 0.98 ms instead of 1.09.
 //
 // Rounded to bf16: the expanded keys and values, as a model that keeps them would
 // round them (a workspace in fp32 would double the bytes and put the products on
@@ -35,7 +36,7 @@
 // the output's own rounding 0.0017, from V's as much, from K's and P's 0.0010
 // each; it falls with the context's length (0.0019 at 16K).
 //
-// The CUDA-core kernels of the same steps take 260 ms where these take 1.07.
+// The CUDA-core kernels of the same steps took 260 ms where these take 1.05.
 #include <algorithm>
 
 #include "latent_internal.cuh"
@@ -54,7 +55,8 @@ constexpr float kLazy = 8.0f;
 // ---------------------------------------------------------------------------
 // expansion
 // ---------------------------------------------------------------------------
-// warps 0..3 half of the latents' columns and the keys' epilogue, 4..7 the other half and the values', 8 copies, 9 MMA issue
+// warps 0..3 half of the latents' columns and the keys' epilogue, 4..7 the other half and the values', 8 copies, 9 MMA
+// issue
 constexpr int kExpThreads = 320;
 constexpr int kHalf = kN / 2;        // a unit's product is taken in two halves, the keys and the values
 constexpr int kStageK = 128;         // reduction width of a stage of weights
@@ -292,7 +294,7 @@ __global__ void __launch_bounds__(kExpThreads, 1)
     // buffers' place), eight lanes a 128-byte line, 64 columns at a time and one
     // step ahead; the lines are asked into L2 all at once before (for the next
     // tile while this one's products run).  Each thread reading its own slot's
-    // row took 10 us a tile, five units' time.
+    // row took 10 us a tile, four units' time.
     auto place = [&](const ExpWalk& w, bool report) -> const uint4* {
       const int slot = w.tile * kSlotTile + row;
       if (slot >= w.end) return nullptr;
@@ -384,7 +386,8 @@ __global__ void __launch_bounds__(kExpThreads, 1)
     };
     // the next tile's latents, once every product of this one is complete
     auto reload = [&](const ExpWalk& next, int n) -> bool {
-      if (store) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // (they pass through the stores' place)
+      // (they pass through the stores' place)
+      if (store) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
       bar_sync(1 + half, 128);
       return load(next, n);
     };
