@@ -39,9 +39,10 @@
 // on the parts that have landed.
 //
 // Whole calls, the join included: 97 us for 96 requests x 128 heads x 2048 listed
-// slots (560 TFLOP/s, 2.6 TB/s).  There a tile takes some 3000 cycles where its
-// products take 1970: a tile's stay in shared memory (copy 1300, S 1200, softmax 1150, second
-// product 780) over the two that fit beside 72 KB of queries.  61 us for 32
+// slots (560 TFLOP/s, 2.6 TB/s).  There a tile takes 2960 cycles.  Its products
+// read both operands from shared memory, 144 KB for S and 96 KB for the second, and 72 KB
+// come in: 2440 cycles at 128 bytes each; the rest is the chain copy, S, softmax,
+// second product of the two tiles that fit beside 72 KB of queries.  61 us for 32
 // requests x 4 rows x 16 heads x 2048 slots, 5.0 TB/s, in steady state at HBM's
 // rate, then the start (7 us of dependent reads: length, list, page, entry) and
 // the outputs.  The CUDA-core kernel takes 14.5 ms for the first.
