@@ -29,7 +29,8 @@ def _expected_bytes(H, dc, dr, dn, dv, cap, el):
     a = lambda x: (x + 255) // 256 * 256
     heads = max(2 * 148 * min(64, -(-H // 16) * 16), 2 * 296 * 8)  # shares: two per block, of the larger kernel
     parts = 148 * 256 if cap else 0  # rows of the expanded form's parts, in the same place
-    return a(16) + a(64 * 8) + a(max(heads, parts) * 8) + a(max(heads * dc, parts * dv) * 4) + a(cap * H * (dn + dv) * el) + a(cap * dr * el)
+    return a(16) + a(64 * 8) + a(max(heads, parts) * 8) + a(max(heads * dc, parts * dv) * 4) + a(cap * H * (dn + dv) * el) + a(cap * dr * el) \
+        + a(cap // 128 * H * 4)
 
 
 @pytest.mark.parametrize("over", [{}, {"num_heads": 128}, {"num_heads": 1}, {"bf16": False}, {"prefill_slots": 0},
