@@ -495,8 +495,9 @@ typedef struct spin_latent_s* spin_latent;
 
 /* Bytes of device memory a handle needs: the error word, the rotary
  * frequencies, the partial sums of a context that several thread blocks share,
- * and for prefill_slots > 0 the expanded keys and values (prefill_slots * (num_heads * (nope_dim + v_dim) +
- * rope_dim) elements).  Returns 0 for an invalid config. */
+ * and for prefill_slots > 0 the expanded keys and values (prefill_slots *
+ * (num_heads * (nope_dim + v_dim) + rope_dim) elements, and num_heads int32 for
+ * every 128 slots).  Returns 0 for an invalid config. */
 SPIN_API size_t spin_latent_bytes(const spin_latent_config* cfg);
 
 /* Creates a handle over the caller's device block dev_mem (>=
@@ -564,7 +565,7 @@ SPIN_API spin_status spin_latent_attention(spin_latent lt, int rows, const void*
  *   w_kv [num_heads][nope_dim + v_dim][latent_dim] contiguous: W_uk then W_uv
  *   of each head;
  *   out [Q][rows][num_heads][v_dim]; rows >= row_count are left as they are.
- * Expanded keys and values are rounded to dtype.  A request whose lengths are
+ * Expanded keys are rounded to dtype, values to dtype or finer.  A request whose lengths are
  * out of range sets ERR_CTX_LEN or ERR_ACCEPTED, one that no longer fits
  * prefill_slots (in request order) ERR_CAPACITY (bit 4), one with a page
  * outside the cache among those of its slots ERR_PAGE; its rows stay

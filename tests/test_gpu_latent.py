@@ -521,7 +521,9 @@ def check_prefill(lt, rows, cache, bt, qv, w, ctx, count, out):
     the reference rounds them too.  Where the kernel's fp32 sum of an expanded
     element lands on the other side of a rounding border, the element differs
     by one step; that happens to a share of about dc 2^-24 / u of them, and
-    the weights' bound below leaves room for it (2-norm: sqrt of that share)."""
+    the weights' bound below leaves room for it (2-norm: sqrt of that share).
+    Values and weights that a kernel keeps finer than dtype differ by the
+    reference's own rounding of the values, within the same bounds."""
     cfg = lt.cfg
     dn, dc = cfg.nope_dim, cfg.latent_dim
     for q in range(cfg.num_requests):
@@ -630,6 +632,23 @@ def test_prefill_refuses_bad_lengths_pages_and_a_full_workspace(dtype):
     got = run_prefill(small, 20, cache, bt, qv, w, ctx, count)
     assert whole(got, 0) and whole(got, 1) and untouched(got, 2) and untouched(got, 3)
     assert isa.spin_latent_error(small) == (6, 16)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("steps", [[40, 40, 40, 40], [-60, -60, -60, -60], [0, 20, 0, -20], [-30, 0, 30, 10], [90, 90, 90, 90]])
+def test_prefill_values_of_any_magnitude(steps, dtype):
+    """Latents times a power of two for each 128 slots, keys' weights divided by
+    the largest, so that logits stay moderate while values leave the range of
+    16-bit formats of few exponent bits."""
+    lt, cache, bt, qv, w, ctx, count = prefill_case(1, 200, 2, [300], None, 64, dtype, 512, 64, 128, 128)
+    s = torch.arange(499, device="cuda")
+    kv = ref.slots_of(cache, bt, 0, s)
+    factor = torch.tensor([2.0 ** e for e in steps], device="cuda", dtype=torch.float64)[s // 128]
+    kv[:, :512] *= factor[:, None]
+    put(cache, bt, 0, s, kv.to(dtype))
+    w[:, :128] *= 2.0 ** -max(steps)
+    out = run_prefill(lt, 200, cache, bt, qv, w, ctx, count)
+    check_prefill(lt, 200, cache, bt, qv, w, ctx, count, out)
 
 
 @pytest.mark.parametrize("Q,fit", [(30, 17), (40, 17), (400, 341)])
