@@ -14,7 +14,7 @@
 //               products:
 //   S_t [128 x 128 keys] = Q_t . K^T   M 128, N 128, K 192 (shared memory both)
 //   O_t [128 x 128]     += P_t . V     M 128, N 128, K 128 (P from TMEM)
-//               P (fp16) overwrites its S in TMEM.  A thread owns a row, so
+//               P (bf16) overwrites its S in TMEM.  A thread owns a row, so
 //               maximum, sum and rescaling need no exchange; the softmax
 //               reference moves only where a row's maximum has grown by more
 //               than 8 (log2 units), and then its warp rescales O.  K and V come
@@ -28,15 +28,15 @@
 //               of its S, and TMEM has no room for another.  Without the softmax
 //               the call took 0.98 ms instead of 1.09.
 //
-// Rounded: the expanded keys to bf16, as the products with bf16 queries ask (half
-// a step, 2^-8); the expanded values and the weights P to fp16, 2^-11, which the
-// second product takes at the same rate.  fp16's range is kept by a power of two
-// for each slot tile and head: the values' largest is stored as 2^14 .. 2^15 and
-// the weights carry the factor.  (Values of a tile that are 2^28 and more below
-// its largest lose bits.)  The sums of the weights are of the unrounded ones, all
-// sums fp32.  With both in bf16 the 2-norm of the error was up to 0.0034 of the
-// output's on some tens of tokens; so it is 0.0024, 0.0017 of it from the
-// output's own rounding.
+// Rounded to bf16, each at most half a step, 2^-8: the expanded keys and values,
+// as a model that keeps them would round them, and the weights P for the second
+// product.  The sums of the weights are of the unrounded ones, all sums fp32.  On
+// some tens of tokens the 2-norm of the error is up to 0.0034 of the output's,
+// 0.0017 of it from the output's own rounding, as much from V's; it falls with the
+// context's length.  fp16 would take less (0.0024), but holds values of any
+// magnitude only with a factor, which a row would share with slots that it does
+// not see or hardly weighs: its own values and weights then fall below fp16's
+// smallest where such a slot is some 2^14 times larger.
 //
 // The CUDA-core kernels of the same steps took 260 ms where these take 1.05.
 #include <algorithm>
@@ -73,7 +73,6 @@ struct ExpMisc {
   uint64_t dfull[2], dfree[2];       // accumulators
   uint64_t done;
   int tmp[35];
-  alignas(16) uint32_t top[2][4];    // the values' largest, by warp, by turns of units
   uint8_t odd[2][kRowTile];          // the first half of a latent's columns is not all finite; by turns of tiles
   uint32_t tmem;
   int abort_flag;
@@ -413,55 +412,33 @@ __global__ void __launch_bounds__(kExpThreads, 1)
         mine = reload(next, nload + 1);
         ask_behind(next, i + 1);
       }
-      uint32_t v[kHalf / 32][32];
-#pragma unroll
-      for (int c = 0; c < kHalf / 32; ++c) tmem_ld32(tmem + lanes + (uint32_t)(half * kHalf + c * 32), v[c]);
-      tmem_wait_ld();
-      // the accumulator is in registers: hand it back
-      fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(ms.dfree[half]));
-      // Values go out as fp16, times a power of two that brings the tile's largest to 2^14 .. 2^15.
-      float scale = 1.f;
-      if (half) {
-        float most = 0.f;
-#pragma unroll
-        for (int c = 0; c < kHalf / 32; ++c)
-#pragma unroll
-          for (int k = 0; k < 32; k += 2)
-            most = max3(most, fabsf(__uint_as_float(v[c][k])), fabsf(__uint_as_float(v[c][k + 1])));
-        const uint32_t mine = __reduce_max_sync(0xffffffffu, clear ? 0u : __float_as_uint(most));
-        if (lane == 0) ms.top[i & 1][warp & 3] = mine;
-        bar_sync(1 + half, 128);
-        const uint4 t = *reinterpret_cast<const uint4*>(ms.top[i & 1]);
-        const int e = min(max((int)(max(max(t.x, t.y), max(t.z, t.w)) >> 23) - 127 - 14, -100), 113);
-        scale = __uint_as_float((uint32_t)(127 - e) << 23);
-        if (store) a.v_exp[w.h * (a.cap / kSlotTile) + w.off / kSlotTile + w.tile] = e;
-      }
-#pragma unroll
+#pragma unroll 1
       for (int c = 0; c < kHalf / 64; ++c) {
+        uint32_t v[2][32];
+        tmem_ld32(tmem + lanes + (uint32_t)(half * kHalf + c * 64), v[0]);
+        tmem_ld32(tmem + lanes + (uint32_t)(half * kHalf + c * 64 + 32), v[1]);
+        tmem_wait_ld();
+        if (c == kHalf / 64 - 1) {  // the accumulator is in registers: hand it back
+          fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(ms.dfree[half]));
+        }
         // the block's buffer: its store two blocks ago has read it
         if (store) asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kOutBufs - 1) : "memory");
         bar_sync(1 + half, 128);
         const uint32_t out = o_at + (half * kOutBufs + buf) * kBlk, dst = out + row * 128;
-        auto write = [&](auto pack) {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            uint32_t p[4];
+        for (int j = 0; j < 8; ++j) {
+          uint32_t p[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int x = 64 * c + 8 * j + 2 * e;
-              p[e] = pack(__uint_as_float(v[x >> 5][x & 31]), __uint_as_float(v[x >> 5][(x & 31) + 1]));
-            }
-            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + ((j ^ (row & 7)) << 4)), "r"(p[0]),
-                         "r"(p[1]), "r"(p[2]), "r"(p[3])
-                         : "memory");
+          for (int e = 0; e < 4; ++e) {
+            const int x = 8 * j + 2 * e;
+            p[e] = clear ? 0u : pack_bf16(__uint_as_float(v[x >> 5][x & 31]), __uint_as_float(v[x >> 5][(x & 31) + 1]));
           }
-        };
-        if (half)
-          write([&](float lo, float hi) { return clear ? 0u : pack_fp16(lo * scale, hi * scale); });
-        else
-          write([&](float lo, float hi) { return pack_bf16(lo, hi); });
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + ((j ^ (row & 7)) << 4)), "r"(p[0]),
+                       "r"(p[1]), "r"(p[2]), "r"(p[3])
+                       : "memory");
+        }
         fence_async_smem();
         bar_sync(1 + half, 128);
         if (store) {
@@ -716,7 +693,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
     // instructions run.
     const int t = warp - 9, nt = t ? n1 : n0;
     const uint32_t id_s = idesc_bf16(128, 128, 0, 0);
-    const uint32_t id_o = idesc_fp16(128, 128, 0, 1);
+    const uint32_t id_o = idesc_bf16(128, 128, 0, 1);
     const uint32_t s_col = tmem + t * 128, o_col = tmem + kOCol + t * 128;
     const uint64_t ad = sw128_desc(q_at + t * kKBlocks * kBlk, 16, 1024);
     // The elected lane's parts.  S(i): columns b of K, at ring block s.
@@ -834,15 +811,9 @@ __global__ void __launch_bounds__(kAttThreads, 1)
     const float scale = a.scale_log2;
     float m = -INFINITY, l = 0.f;
     bool ok = true;
-    // The tile's values are stored times 2^-e: the weights for them take the
-    // factor 2^e along, so that what counts in O lies near 1 (reference m is of
-    // logit + e), and their sum gives it back.
-    const int32_t* v_exp = a.v_exp + h * (a.cap / kSlotTile) + off / kSlotTile + i0;
-    float e = 0.f;
     // halves of 64 keys
     for (int j = 0; j < 2 * nt; ++j) {
       const uint32_t at = s_at + (j & 1) * 64;
-      if (!(j & 1)) e = (float)v_exp[j >> 1];
       // (S of a key tile follows the second products of the tile before)
       if (!(j & 1)) ok = wait_warp(bar(ms.sfull[t]), (uint32_t)(j >> 1) & 1u, ctl);
       if (!ok) break;
@@ -863,7 +834,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
 #pragma unroll
         for (int k = 0; k < 4; ++k)
           mt[k] = max3(mt[k], __uint_as_float(s[0][c + k]), __uint_as_float(s[1][c + k]));
-      const float top = fmaxf(fmaxf(mt[0], mt[1]), fmaxf(mt[2], mt[3])) * scale + e;
+      const float top = fmaxf(fmaxf(mt[0], mt[1]), fmaxf(mt[2], mt[3])) * scale;
       if (__any_sync(0xffffffffu, top > m + kLazy)) {  // (true at the first half: m is -inf)
         const float mn = fmaxf(m, top);
         const float f = mn == -INFINITY ? 1.f : ex2(m - mn);
@@ -885,7 +856,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
           }
         }
       }
-      const float ref = m == -INFINITY ? 0.f : m - e;
+      const float ref = m == -INFINITY ? 0.f : m;
       float sum[4] = {0.f, 0.f, 0.f, 0.f};
       uint32_t p[32];
 #pragma unroll
@@ -900,7 +871,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
           x[k] = ex2(x[k]);
           x[k + 1] = ex2(x[k + 1]);
           add2(sum[k], sum[k + 1], x[k], x[k + 1]);
-          p[c + k / 2] = pack_fp16(x[k], x[k + 1]);
+          p[c + k / 2] = pack_bf16(x[k], x[k + 1]);
         }
       }
       tmem_st32(at, p);
@@ -908,7 +879,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
       fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(ms.pfull[t][j & 1]));
-      l = fmaf((sum[0] + sum[1]) + (sum[2] + sum[3]), ex2(-e), l);
+      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
     }
     // (a barrier of one phase: the products behind this warp's last weights may be complete before it looks, and
     // odone's parity would not tell)

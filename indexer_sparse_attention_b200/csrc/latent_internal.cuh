@@ -266,7 +266,6 @@ struct PrefillArgs {
   void* out;                 // [Q][rows][H][dv]
   void* kv;                  // [H][cap][dn + dv]
   void* kr;                  // [cap][dr]
-  int32_t* v_exp;            // tensor-core kernel: [H][cap / 128], a slot tile's values are stored times 2^-v_exp
   float* part;               // tensor-core kernel: parts cut along the keys, [148][256][dv]
   float2* part_ml;           // [148][256] (maximum in log2 units, sum)
   int planned;               // tensor-core kernel: few enough rows to rank and cut

@@ -4,7 +4,6 @@
 #pragma once
 
 #include <cuda.h>
-#include <cuda_fp16.h>
 
 #include "spin_internal.cuh"
 
@@ -153,7 +152,7 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 // ---------------------------------------------------------------------------
-// tcgen05.mma, kind::f16: both operands bf16 or both fp16, fp32 accumulators
+// tcgen05.mma, kind::f16 with bf16 operands and fp32 accumulators
 // ---------------------------------------------------------------------------
 // Shared-memory descriptor of a 128-byte-swizzled operand (8-row atoms of
 // 1024 bytes).  K-major: rows are M (or N), 64 elements of K wide; `lbo` is
@@ -168,11 +167,6 @@ __device__ __forceinline__ uint64_t sw128_desc(uint32_t saddr, uint32_t lbo, uin
 __host__ __device__ constexpr uint32_t idesc_bf16(int M, int N, int a_mn, int b_mn) {
   return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)a_mn << 15) | ((uint32_t)b_mn << 16) |
          ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
-}
-// D fp32, A and B fp16.
-__host__ __device__ constexpr uint32_t idesc_fp16(int M, int N, int a_mn, int b_mn) {
-  return (1u << 4) | ((uint32_t)a_mn << 15) | ((uint32_t)b_mn << 16) | ((uint32_t)(N >> 3) << 17) |
-         ((uint32_t)(M >> 4) << 24);
 }
 __device__ __forceinline__ void mma_f16(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
   asm volatile(
@@ -287,12 +281,6 @@ __device__ __forceinline__ float ex2(float x) {
 }
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-  uint32_t u;
-  memcpy(&u, &v, 4);
-  return u;
-}
-__device__ __forceinline__ uint32_t pack_fp16(float lo, float hi) {
-  const __half2 v = __floats2half2_rn(lo, hi);
   uint32_t u;
   memcpy(&u, &v, 4);
   return u;

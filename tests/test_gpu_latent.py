@@ -651,6 +651,53 @@ def test_prefill_values_of_any_magnitude(steps, dtype):
     check_prefill(lt, 200, cache, bt, qv, w, ctx, count, out)
 
 
+def check_first_rows(lt, cache, bt, qv, w, ctx, out, n):
+    """The first n[q] rows of each request against 64 bits."""
+    head = out.clone()
+    for q, k in enumerate(n):
+        head[q, k:] = 7
+    check_prefill(lt, qv.shape[1], cache, bt, qv, w, ctx, ints(n), head)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("ctx0", [100, 3000])
+@pytest.mark.parametrize("power", [8, 14, 18, 24, 30, 40, 60, 100])
+def test_prefill_rows_before_a_large_token(power, ctx0, dtype):
+    """One token of the chunk 2^power times as large as the others: the rows
+    before it, those of its own 128 slots too, are as near to 64 bits as
+    without it."""
+    lt, cache, bt, qv, w, ctx, count = prefill_case(2, 200, 2, [ctx0, 40], [200, 130], 64, dtype, 512, 64, 128, 128)
+    for row in (60, 199):
+        slot = ints([ctx0 - 1 + row]).long()
+        kept = ref.slots_of(cache, bt, 0, slot)
+        large = kept.clone()
+        large[:, :512] *= 2.0 ** power
+        put(cache, bt, 0, slot, large.to(dtype))
+        out = run_prefill(lt, 200, cache, bt, qv, w, ctx, count)
+        check_first_rows(lt, cache, bt, qv, w, ctx, out, [row, 130])
+        put(cache, bt, 0, slot, kept.to(dtype))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("ctx0", [300, 3000])
+@pytest.mark.parametrize("power", [12, 16, 20, 24, 28, 40])
+def test_prefill_a_large_value_of_hardly_any_weight(power, ctx0, dtype):
+    """A token of the context whose values are 2^power times the others' and
+    whose weight is e^-46 of theirs (2^-66): at most 2^-26 of an output comes
+    from it, and the other tokens keep their precision.  Keys are the rotary
+    parts alone: q . k is 64 of the first token's -10 and about 0 of the others."""
+    lt, cache, bt, qv, w, ctx, count = prefill_case(1, 150, 2, [ctx0], None, 64, dtype, 512, 64, 128, 128)
+    w[:, :128] = 0
+    qv[..., 128:] = 1
+    slot = ints([17]).long()
+    kv = ref.slots_of(cache, bt, 0, slot)
+    kv[:, :512] *= 2.0 ** power
+    kv[:, 512:] = -10
+    put(cache, bt, 0, slot, kv.to(dtype))
+    out = run_prefill(lt, 150, cache, bt, qv, w, ctx, count)
+    check_prefill(lt, 150, cache, bt, qv, w, ctx, count, out)
+
+
 @pytest.mark.parametrize("Q,fit", [(30, 17), (40, 17), (400, 341)])
 def test_prefill_of_many_requests_in_a_workspace_for_some(Q, fit):
     """Requests of two slot tiles each, in order: those behind the first that does not fit stay unwritten."""
