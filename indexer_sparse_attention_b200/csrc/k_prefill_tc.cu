@@ -53,6 +53,7 @@ constexpr int kDC = 512, kDR = 64, kDN = 128, kDV = 128, kN = kDN + kDV;
 constexpr int kRowTile = 128;
 constexpr int kBlk = kRowTile * 128;  // 128 rows of 64 columns
 constexpr float kLazy = 8.0f;
+constexpr int kNoSlot = 0x7fffffff;
 
 // ---------------------------------------------------------------------------
 // expansion
@@ -73,7 +74,7 @@ struct ExpMisc {
   uint64_t dfull[2], dfree[2];       // accumulators
   uint64_t done;
   int tmp[35];
-  uint8_t odd[2][kRowTile];          // the first half of a latent's columns is not all finite; by turns of tiles
+  alignas(16) int odd[2][4];         // first slot of a warp whose values are not all finite; by turns of units
   uint32_t tmem;
   int abort_flag;
 };
@@ -286,11 +287,7 @@ __global__ void __launch_bounds__(kExpThreads, 1)
     const LatentCache& C = a.cache;
     // A slot tile's latents: a thread's slot into its TMEM lane, two elements a
     // column.  Slots past the request's last become zeros, and so do their keys
-    // and values: a weight of 0 must meet no NaN.  The rotary part goes
-    // straight to the workspace.  Returns whether this half of the slot's latent holds what
-    // is not finite: the slot's values are then written as zeros, so that rows before
-    // the slot, whose weights for it are 0, stay clean; rows that attend to it
-    // see the keys made of it.
+    // and values.  The rotary part goes straight to the workspace.
     // Each half of the warps takes four of the eight 64-column pieces.
     // A warp brings its 32 slots' pieces by way of shared memory (the output
     // buffers' place), eight lanes a 128-byte line, 64 columns at a time and one
@@ -314,7 +311,7 @@ __global__ void __launch_bounds__(kExpThreads, 1)
       for (int c = 0; c < (kDC + kDR) / 64; ++c)
         asm volatile("prefetch.global.L2 [%0];" ::"l"(src + 8 * c) : "memory");
     };
-    auto load = [&](const ExpWalk& w, int n) -> bool {  // n: the block's n-th tile
+    auto load = [&](const ExpWalk& w) {
       const int slot = w.tile * kSlotTile + row;
       const uint4* src = place(w, true);
       ask(src);
@@ -336,7 +333,6 @@ __global__ void __launch_bounds__(kExpThreads, 1)
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
       };
-      __nv_bfloat162 zero = __floats2bfloat162_rn(0.f, 0.f), probe = zero;  // sum of 0 x: 0 or NaN
       constexpr int kPieces = kDC / 64 / 2;
       fetch(half * kPieces);
 #pragma unroll 1
@@ -356,16 +352,8 @@ __global__ void __launch_bounds__(kExpThreads, 1)
                        : "r"(stage + (c & 1) * kBlk + lane * 128 + ((k ^ (lane & 7)) << 4))
                        : "memory");
         tmem_st32(tmem + lanes + kACol + (uint32_t)c * 32, v);
-#pragma unroll
-        for (int k = 0; k < 32; ++k) {
-          __nv_bfloat162 e;
-          memcpy(&e, &v[k], 4);
-          probe = __hfma2(e, zero, probe);
-        }
         __syncwarp();  // the buffer has been read
       }
-      const bool odd = !(__low2float(probe) == 0.f && __high2float(probe) == 0.f);
-      if (!half) ms.odd[n & 1][row] = odd;
       tmem_wait_st();
       fence_before();
       __syncwarp();
@@ -377,7 +365,6 @@ __global__ void __launch_bounds__(kExpThreads, 1)
           *reinterpret_cast<uint4*>(dst + j * (4 * kDR * 2)) =
               from[j] ? *reinterpret_cast<const uint4*>(from[j] + kDC * 2 + (lane & 7) * 16) : make_uint4(0, 0, 0, 0);
       }
-      return odd;
     };
     const bool store = (threadIdx.x & 127) == 0;  // the half's thread that issues its stores
     auto ask_behind = [&](ExpWalk at, int unit) {  // the tile behind that of `at`, the block's unit `unit`
@@ -387,20 +374,16 @@ __global__ void __launch_bounds__(kExpThreads, 1)
       ask(place(at, false));
     };
     // the next tile's latents, once every product of this one is complete
-    auto reload = [&](const ExpWalk& next, int n) -> bool {
+    auto reload = [&](const ExpWalk& next) {
       // (they pass through the stores' place)
       if (store) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
       bar_sync(1 + half, 128);
-      return load(next, n);
+      load(next);
     };
-    int buf = 0, nload = 0;
-    bool mine = load(w, 0), ok = true;
-    bool clear = false;  // this slot's values are written as zeros
-    if (half) {
-      ask_behind(w, 0);
-      ok = wait_warp(bar(ms.afull), 0, ctl);
-      clear = mine || ms.odd[0][row];
-    }
+    int buf = 0;
+    bool ok = true;
+    load(w);
+    if (half) ask_behind(w, 0);
     for (int i = 0; i < n_units; ++i) {
       ok = ok && wait_warp(bar(ms.dfull[half]), (uint32_t)i & 1u, ctl);
       if (bar_or(1 + half, 128, !ok)) break;  // (the warps leave together: they meet at barriers below)
@@ -409,9 +392,10 @@ __global__ void __launch_bounds__(kExpThreads, 1)
       if (i + 1 < n_units) next.step(a);
       const bool turn = next.tile != w.tile || next.q != w.q;
       if (half && turn) {  // before the epilogue, so that the next products begin
-        mine = reload(next, nload + 1);
+        reload(next);
         ask_behind(next, i + 1);
       }
+      bool odd = false;  // of the values, not all are finite
 #pragma unroll 1
       for (int c = 0; c < kHalf / 64; ++c) {
         uint32_t v[2][32];
@@ -423,22 +407,34 @@ __global__ void __launch_bounds__(kExpThreads, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(ms.dfree[half]));
         }
+        uint32_t p[32];
+#pragma unroll
+        for (int k = 0; k < 32; ++k)
+          p[k] = pack_bf16(__uint_as_float(v[k >> 4][2 * k & 31]), __uint_as_float(v[k >> 4][(2 * k & 31) + 1]));
+        // Values that are not finite in bf16 are written as zeros: rows before the
+        // slot, whose weights for it are 0, must not meet them.  Rows that attend to
+        // the slot learn of it by the tile's first such slot.
+        if (half) {
+          uint32_t most = 0;
+#pragma unroll
+          for (int k = 0; k < 32; ++k) most = __vmaxu2(most, p[k] & 0x7fff7fffu);
+          const bool clear = (most & 0xffffu) >= 0x7f80u || most >> 16 >= 0x7f80u;
+          if (clear)
+#pragma unroll
+            for (int k = 0; k < 32; ++k) p[k] = 0;
+          odd |= clear;
+          const uint32_t who = __ballot_sync(0xffffffffu, odd);
+          if (lane == 0) ms.odd[i & 1][warp & 3] = who ? w.tile * kSlotTile + row + __ffs((int)who) - 1 : kNoSlot;
+        }
         // the block's buffer: its store two blocks ago has read it
         if (store) asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kOutBufs - 1) : "memory");
         bar_sync(1 + half, 128);
         const uint32_t out = o_at + (half * kOutBufs + buf) * kBlk, dst = out + row * 128;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          uint32_t p[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int x = 8 * j + 2 * e;
-            p[e] = clear ? 0u : pack_bf16(__uint_as_float(v[x >> 5][x & 31]), __uint_as_float(v[x >> 5][(x & 31) + 1]));
-          }
-          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + ((j ^ (row & 7)) << 4)), "r"(p[0]),
-                       "r"(p[1]), "r"(p[2]), "r"(p[3])
+        for (int j = 0; j < 8; ++j)
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + ((j ^ (row & 7)) << 4)), "r"(p[4 * j]),
+                       "r"(p[4 * j + 1]), "r"(p[4 * j + 2]), "r"(p[4 * j + 3])
                        : "memory");
-        }
         fence_async_smem();
         bar_sync(1 + half, 128);
         if (store) {
@@ -450,16 +446,16 @@ __global__ void __launch_bounds__(kExpThreads, 1)
         }
         buf ^= 1;
       }
-      if (turn) {
+      if (half && store) {
+        const int4 first = *reinterpret_cast<const int4*>(ms.odd[i & 1]);
+        a.odd[w.h * (a.cap / kSlotTile) + w.off / kSlotTile + w.tile] =
+            min(min(first.x, first.y), min(first.z, first.w));
+      }
+      if (turn && !half) {
         // (of the keys' warps the epilogue comes first: the values' products run meanwhile)
-        ++nload;
-        ok = half ? wait_warp(bar(ms.afull), (uint32_t)nload & 1u, ctl)
-                  : wait_warp(bar(ms.dfull[1]), (uint32_t)i & 1u, ctl);
+        ok = wait_warp(bar(ms.dfull[1]), (uint32_t)i & 1u, ctl);
         if (bar_or(1 + half, 128, !ok)) break;
-        if (half)
-          clear = mine || ms.odd[nload & 1][row];
-        else
-          reload(next, nload);
+        reload(next);
       }
       w = next;
     }
@@ -811,9 +807,13 @@ __global__ void __launch_bounds__(kAttThreads, 1)
     const float scale = a.scale_log2;
     float m = -INFINITY, l = 0.f;
     bool ok = true;
+    // The first slot whose values are not finite (they are stored as zeros): a row that sees it becomes NaN.
+    const int32_t* odd = a.odd + h * (a.cap / kSlotTile) + off / kSlotTile + i0;
+    int spoilt = kNoSlot, first_odd = kNoSlot;
     // halves of 64 keys
     for (int j = 0; j < 2 * nt; ++j) {
       const uint32_t at = s_at + (j & 1) * 64;
+      if (!(j & 1)) first_odd = odd[j >> 1];
       // (S of a key tile follows the second products of the tile before)
       if (!(j & 1)) ok = wait_warp(bar(ms.sfull[t]), (uint32_t)(j >> 1) & 1u, ctl);
       if (!ok) break;
@@ -880,7 +880,9 @@ __global__ void __launch_bounds__(kAttThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(ms.pfull[t][j & 1]));
       l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      spoilt = min(spoilt, first_odd);
     }
+    if (spoilt <= pos0 + t * kRowTile + tid) l = __int_as_float(0x7fffffff);
     // (a barrier of one phase: the products behind this warp's last weights may be complete before it looks, and
     // odone's parity would not tell)
     if (ok && nt) ok = wait_warp(bar(ms.olast[t]), 0, ctl);

@@ -20,6 +20,7 @@ struct spin_latent_s {
   float* part;
   void* kv;
   void* kr;
+  int32_t* odd;
   RopeTable rope;
   void* encode_fn;  // cuTensorMapEncodeTiled
   uint32_t magic;
@@ -87,7 +88,7 @@ bool valid_config(const spin_latent_config* c) {
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 struct Carve {
-  size_t err, turn, ml, part, kv, kr, flags, total;
+  size_t err, turn, ml, part, kv, kr, odd, total;
 };
 
 Carve carve(const spin_latent_config* c) {
@@ -112,7 +113,7 @@ Carve carve(const spin_latent_config* c) {
   k.part = take(std::max(heads * c->latent_dim, parts * c->v_dim) * sizeof(float));
   k.kv = take(c->prefill_slots ? (size_t)c->prefill_slots * c->num_heads * (c->nope_dim + c->v_dim) * el : 0);
   k.kr = take(c->prefill_slots ? (size_t)c->prefill_slots * c->rope_dim * el : 0);
-  k.flags = take(c->prefill_slots ? (size_t)c->prefill_slots / kSlotTile * c->num_heads * sizeof(int32_t) : 0);
+  k.odd = take(c->prefill_slots ? (size_t)c->prefill_slots / kSlotTile * c->num_heads * sizeof(int32_t) : 0);
   k.total = off;
   return k;
 }
@@ -203,6 +204,7 @@ spin_status spin_latent_create(const spin_latent_config* cfg, void* dev_mem, siz
   lt->part = (float*)(lt->base + k.part);
   lt->kv = lt->base + k.kv;
   lt->kr = lt->base + k.kr;
+  lt->odd = (int32_t*)(lt->base + k.odd);
   const RopeValues rope = rope_values(*cfg);
   lt->rope.turn = (const uint64_t*)(lt->base + k.turn);
   lt->rope.mul = rope.mul;
@@ -404,6 +406,7 @@ spin_status spin_latent_prefill(spin_latent lt, int rows, const void* cache, int
   a.out = out;
   a.kv = lt->kv;
   a.kr = lt->kr;
+  a.odd = lt->odd;
   a.part = lt->part;
   a.part_ml = lt->part_ml;
   a.scale_log2 = (float)((double)c.softmax_scale * 1.4426950408889634);

@@ -266,6 +266,7 @@ struct PrefillArgs {
   void* out;                 // [Q][rows][H][dv]
   void* kv;                  // [H][cap][dn + dv]
   void* kr;                  // [cap][dr]
+  int32_t* odd;              // tensor-core kernel: [H][cap / 128], a tile's first slot with values that are not finite
   float* part;               // tensor-core kernel: parts cut along the keys, [148][256][dv]
   float2* part_ml;           // [148][256] (maximum in log2 units, sum)
   int planned;               // tensor-core kernel: few enough rows to rank and cut

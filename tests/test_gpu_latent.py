@@ -698,6 +698,35 @@ def test_prefill_a_large_value_of_hardly_any_weight(power, ctx0, dtype):
     check_prefill(lt, 150, cache, bt, qv, w, ctx, count, out)
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("H,ctx0", [(2, 100), (1, 3000), (60, 300)])
+def test_prefill_rows_before_finite_latents_whose_values_are_not(H, ctx0, dtype):
+    """Latents of 2^127 (finite), value weights that sum them past the dtype's
+    range in one element of every head (all 512 of one sign) and on the way, by
+    signs in turn, in another, and keys of 0: the rows before have the bits that
+    they had, those that see the slot are not finite in the first element."""
+    lt, cache, bt, qv, w, ctx, count = prefill_case(2, 200, H, [ctx0, 40], [200, 130], 64, dtype, 512, 64, 128, 128)
+    w[:, :128] = 0
+    out = run_prefill(lt, 200, cache, bt, qv, w, ctx, count)
+    check_prefill(lt, 200, cache, bt, qv, w, ctx, count, out)
+    slots = [ctx0 - 1 + row for row in (70, 131, 199)]
+    for column in (128, 200, 255):
+        w2 = w.clone()
+        w2[:, column] = 1
+        w2[:, column ^ 1, ::2], w2[:, column ^ 1, 1::2] = 1, -1
+        base = run_prefill(lt, 200, cache, bt, qv, w2, ctx, count)
+        for slot in slots:
+            broken = cache.clone()
+            kv = ref.slots_of(cache, bt, 0, ints([slot]).long())
+            kv[:, :512] = 2.0 ** 127
+            put(broken, bt, 0, ints([slot]).long(), kv.to(dtype))
+            got = run_prefill(lt, 200, broken, bt, qv, w2, ctx, count)
+            row = slot - (ctx0 - 1)
+            assert torch.equal(got[0, :row], base[0, :row]) and torch.equal(got[1], base[1])
+            assert not torch.isfinite(got[0, row:, :, column - 128]).any()
+    assert isa.spin_latent_error(lt) == (0, 0)
+
+
 @pytest.mark.parametrize("Q,fit", [(30, 17), (40, 17), (400, 341)])
 def test_prefill_of_many_requests_in_a_workspace_for_some(Q, fit):
     """Requests of two slot tiles each, in order: those behind the first that does not fit stay unwritten."""
