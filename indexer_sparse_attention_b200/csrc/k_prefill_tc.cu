@@ -835,9 +835,12 @@ __global__ void __launch_bounds__(kAttThreads, 1)
         for (int k = 0; k < 4; ++k)
           mt[k] = max3(mt[k], __uint_as_float(s[0][c + k]), __uint_as_float(s[1][c + k]));
       const float top = fmaxf(fmaxf(mt[0], mt[1]), fmaxf(mt[2], mt[3])) * scale;
-      if (__any_sync(0xffffffffu, top > m + kLazy)) {  // (true at the first half: m is -inf)
-        const float mn = fmaxf(m, top);
-        const float f = mn == -INFINITY ? 1.f : ex2(m - mn);
+      // (at the first half m is -inf; a row's reference moves by its own maximum alone, so that its bits do not
+      // depend on what its warp's other rows see)
+      const bool grown = top > m + kLazy;
+      if (__any_sync(0xffffffffu, grown)) {
+        const float mn = grown ? top : m;
+        const float f = grown ? ex2(m - mn) : 1.f;
         m = mn;
         l *= f;
         if (j > 0) {

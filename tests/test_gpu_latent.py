@@ -727,6 +727,24 @@ def test_prefill_rows_before_finite_latents_whose_values_are_not(H, ctx0, dtype)
     assert isa.spin_latent_error(lt) == (0, 0)
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("ctx0", [100, 3000])
+@pytest.mark.parametrize("power", [3, 8, 20, 100])
+def test_prefill_rows_have_the_same_bits_whatever_comes_behind_them(power, ctx0, dtype):
+    """A token of other latents, 2^power times as large, and another query of a
+    later row: logits of the rows behind rise, those before keep their bits."""
+    lt, cache, bt, qv, w, ctx, count = prefill_case(2, 200, 2, [ctx0, 40], [200, 130], 64, dtype, 512, 64, 128, 128)
+    out = run_prefill(lt, 200, cache, bt, qv, w, ctx, count)
+    for row in (5, 50, 113, 199):
+        slot, broken, q2 = ints([ctx0 - 1 + row]).long(), cache.clone(), qv.clone()
+        put(broken, bt, 0, slot, (randn(gen(row), 1, 576, dtype=F32) * 2.0 ** power).to(dtype))
+        got = run_prefill(lt, 200, broken, bt, qv, w, ctx, count)
+        assert torch.equal(got[0, :row], out[0, :row]) and torch.equal(got[1], out[1]), row
+        q2[0, row] *= 2.0 ** power
+        got = run_prefill(lt, 200, cache, bt, q2, w, ctx, count)
+        assert torch.equal(got[0, :row], out[0, :row]) and torch.equal(got[0, row + 1:], out[0, row + 1:]), row
+
+
 @pytest.mark.parametrize("Q,fit", [(30, 17), (40, 17), (400, 341)])
 def test_prefill_of_many_requests_in_a_workspace_for_some(Q, fit):
     """Requests of two slot tiles each, in order: those behind the first that does not fit stay unwritten."""
