@@ -333,7 +333,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      landed(B.qfull);
+      if (a.q_vec) {
+        landed(B.qfull);
+      } else {  // plain stores: no asynchronous arrival stands for them, and the product reads through the async proxy
+        fence_async_smem();
+        mbar_arrive(bar(B.qfull));
+      }
     };
     queries(w.item);
     int seg = 0, flags = 0;

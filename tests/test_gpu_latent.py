@@ -373,6 +373,20 @@ def test_attention_takes_strided_and_unaligned_queries(dtype):
     assert torch.equal(got[0], full[0])
 
 
+@pytest.mark.parametrize("Q,rows,H,topk", [(1, 1, 16, 64), (200, 2, 16, 130), (160, 1, 128, 64), (9, 4, 40, 0)])
+def test_attention_unaligned_queries_of_many_items_a_block(Q, rows, H, topk):
+    """The first item of a block and those behind it, over and over."""
+    lt, cache, bt, ql, qr, ctx, topk = attention_case(Q, rows, H, topk, [150 + 7 * q % 400 for q in range(Q)], 64, BF16,
+                                                      512, 64)
+    out, lse = run_attention(lt, rows, cache, bt, ql, qr, ctx, topk)
+    room = torch.full((Q * rows * H * 579 + 1,), math.nan, dtype=BF16, device="cuda")[1:].view(Q, rows, H, 579)
+    room[..., :512], room[..., 512:576] = ql, qr
+    for _ in range(20):
+        got = run_attention(lt, rows, cache, bt, room[..., :512], room[..., 512:576], ctx, topk)
+        assert torch.equal(got[0], out) and torch.equal(got[1], lse)
+    assert isa.spin_latent_error(lt) == (0, 0)
+
+
 def test_attention_large_logits_and_one_sided_weights():
     """Weights that all sit on one token, and maxima that rise tile by tile."""
     lt, cache, bt, ql, qr, ctx, _ = attention_case(1, 1, 16, 0, [500], 64, BF16, 512, 64)
