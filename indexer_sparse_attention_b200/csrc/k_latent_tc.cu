@@ -176,12 +176,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(bar(B.oempty), kSoft / 32);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
+  // TMEM is taken behind the wait and held before the release: a kernel that
+  // still waits for the one before never holds columns which that may need, and
+  // its own successor is not there yet.
+  pdl_wait();
   if (warp == kMmaWarp) tmem_alloc(smem_u32(&ms.tmem), kTmemCols);
-  fence_before();
-  __syncthreads();
-  fence_after();
-  const uint32_t tmem = ms.tmem;
-  pdl_enter();
 
   // the block's items and units (all threads)
   Walk w;
@@ -196,8 +195,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       w.stop = range_begin(at.total, at.ranges, u + 1);
     }
     w.item = w.whole ? u * w.whole : w.later;
+    fence_before();
     __syncthreads();
+    fence_after();
   }
+  const uint32_t tmem = ms.tmem;
+  pdl_release();
   const int my_begin = w.at;
   const bool any = w.whole || w.at < w.stop;
 

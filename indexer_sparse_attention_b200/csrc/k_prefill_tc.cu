@@ -137,12 +137,10 @@ __global__ void __launch_bounds__(kExpThreads, 1)
     mbar_init(bar(ms.done), 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
+  // (TMEM behind the wait for the kernel before, whichever that is, and ahead of
+  // the release of the attention, which takes its own before it waits)
+  pdl_wait();
   if (warp == 9) tmem_alloc(smem_u32(&ms.tmem), 512);
-  fence_before();
-  __syncthreads();
-  fence_after();
-  const uint32_t tmem = ms.tmem;
-  pdl_enter();
 
   // This block's units.  Requests in order; one that does not fit the
   // workspace ends the list (those behind it do not fit either).
@@ -207,6 +205,11 @@ __global__ void __launch_bounds__(kExpThreads, 1)
       w.open(a);
     }
   }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = ms.tmem;
+  pdl_release();
 
   if (!n_units) {
     // more blocks than units
@@ -634,6 +637,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
+  // (ahead of the wait: the kernel before is the expansion, which had all its TMEM when it let this one in)
   if (warp == 9) tmem_alloc(smem_u32(&ms.tmem), 512);
   fence_before();
   __syncthreads();

@@ -200,9 +200,11 @@ __device__ __forceinline__ void quantize_vec(const void* q, const float* w, int 
 // ordinary launch), and only then lets its own successor be scheduled, so
 // the stream's ordering is kept for every byte either kernel touches.
 // ---------------------------------------------------------------------------
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void pdl_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void pdl_enter() {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  pdl_wait();
+  pdl_release();
 }
 
 // Launch configuration with programmatic stream serialization; use in place.

@@ -848,6 +848,38 @@ def test_a_layer_with_the_indexers_topk():
     assert isa.spin_latent_error(lt) == (0, 0) and isa.spin_get_error(st) == (0, 0)
 
 
+def test_tensor_core_kernels_of_all_calls_one_behind_the_other():
+    """The indexer's scores, the absorbed and the expanded attention back to
+    back on one stream, each let in before the one before has ended."""
+    Q, H, k = 8, 64, 512
+    g = gen(21)
+    lt, cache, bt, qv, w, ctx, count = prefill_case(Q, 40, H, [900 - 50 * q for q in range(Q)], None, 64, BF16, 512, 64,
+                                                    128, 128, topk=k)
+    st = isa.SpinState(isa.make_config(num_layers=1, num_requests=Q, max_slots=lt.cfg.max_slots, topk=k,
+                                       target_sparsity=0.0))
+    keys = torch.randn((cache.shape[0], 64, 128), generator=g, device="cuda").to(torch.float8_e4m3fn).view(torch.uint8)
+    scale = torch.ones((cache.shape[0], 64), device="cuda")
+    iq, iw = randn(g, Q, 1, 64, 128), torch.rand((Q, 1, 64), generator=g, device="cuda")
+    mask, topk = st.new_mask(), torch.empty((Q, 1, k), dtype=torch.int32, device="cuda")
+    ql, qr = randn(g, Q, 1, H, 512), randn(g, Q, 1, H, 64)
+    out, pre = torch.empty_like(ql), torch.empty((Q, 40, H, 128), dtype=BF16, device="cuda")
+    cache.nan_to_num_(nan=0.25)
+    results = []
+    for step in range(12):
+        for x in (out, pre):
+            x.fill_(math.nan)
+        isa.spin_decode_step(st, 0, 1, step, keys, scale, bt, iq, iw, ctx, False, mask, topk)
+        if step % 3 != 1:
+            isa.spin_latent_attention(lt, 1, cache, bt, ql, qr, ctx, topk, out)
+        isa.spin_latent_prefill(lt, 40, cache, bt, qv, w, ctx, count, pre)
+        if step % 3 == 1:
+            isa.spin_latent_attention(lt, 1, cache, bt, ql, qr, ctx, topk, out)
+        results.append((topk.clone(), out.clone(), pre.clone()))
+    assert all(torch.equal(a, b) for r in results[1:] for a, b in zip(r, results[0]))
+    check_attention(lt, 1, cache, bt, ql, qr, ctx, topk, out, run_attention(lt, 1, cache, bt, ql, qr, ctx, topk)[1])
+    assert isa.spin_latent_error(lt) == (0, 0) and isa.spin_get_error(st) == (0, 0)
+
+
 @pytest.mark.skipif(torch.cuda.device_count() < 2, reason="needs a second device")
 def test_a_handle_of_another_device_than_the_current_one():
     lt = isa.SpinLatent(isa.make_latent_config(num_requests=1, max_slots=64), device="cuda:1")
