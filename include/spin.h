@@ -516,8 +516,9 @@ SPIN_API spin_status spin_latent_destroy(spin_latent lt);
  * positions_dev [tokens] int32, of either sign: -p undoes p (a rotation's
  * transpose), up to attn_factor.  out == x with x's strides rotates in
  * place; any other overlap is not allowed.  heads * head_dim is at most 2^30.
- * Angles are exact to 2^-31 of a turn at every position: the turn's fraction is
- * an integer product modulo 2^64. */
+ * Angles are within 2^-26 of a turn (the fraction of a turn, an integer product
+ * modulo 2^64, as a 32-bit float), and what f_i's own rounding to a double makes
+ * of the position: |position| * f_i * 2^-51 radians at most, 2^-31 at 2^20. */
 SPIN_API spin_status spin_rope(spin_latent lt, int64_t tokens, int heads, int head_dim, int offset, const void* x,
                                int64_t x_token_stride, int64_t x_head_stride, const int32_t* positions_dev,
                                void* out, int64_t out_token_stride, int64_t out_head_stride, spin_stream_t stream);

@@ -12,8 +12,10 @@ namespace spin {
 // Rotary angles.  The turn of pair i at position p is p * f_i / (2 pi), of
 // which only the fraction matters.  With F_i = round(2^64 * frac(f_i / (2
 // pi))) the fraction is p * F_i modulo 2^64: one integer product, wrong by at
-// most |p| * 2^-65 of a turn, at every position and either sign, where an
-// angle in 32-bit floats loses about 2^-24 of p * f_i itself.
+// most |p| * 2^-65 of a turn beside f_i's own rounding (a double: |p| * f_i *
+// 2^-51 radians at most), at every position and either sign, where an angle in
+// 32-bit floats loses about 2^-24 of p * f_i itself.  The fraction as a float
+// costs up to 2^-26 of a turn, half a step of the largest ones.
 // ---------------------------------------------------------------------------
 constexpr int kMaxRopeDim = 128;
 struct RopeTable {

@@ -4,6 +4,7 @@ contexts) and expanded attention of a chunk, over dtypes, widths, head counts,
 lengths, page sizes and strides, with masked places full of NaN, empty rows,
 bad lengths and pages, other streams, captured graphs, and a whole layer run
 with the indexer's own top-k."""
+import decimal
 import math
 
 import pytest
@@ -126,6 +127,32 @@ def test_rope(tokens, heads, head_dim, offset, d, half, dtype, over):
         back = isa.spin_rope(lt, out.clone(), -pos.clamp(min=-2**31 + 1), offset=offset)
         assert (back.double() - x.double()).abs().max() <= (4 * ref.half_step(dtype) + 2.0 ** -18) * x.abs().max()
     assert isa.spin_latent_error(lt) == (0, 0)
+
+
+@pytest.mark.parametrize("base,scaling,factor", [(10000.0, 0, 1.0), (500000.0, 0, 1.0), (10000.0, 1, 40.0)])
+def test_rope_angles_at_any_position(base, scaling, factor):
+    """fp32 at positions over the whole range of int32, against angles from 60
+    decimal digits, to the bound that the header states."""
+    d, tokens = 64, 130
+    g = gen(5)
+    lt = handle(1, 64, rope_dim=d, bf16=False, rope_base=base, rope_scaling=scaling, rope_factor=factor)
+    x = randn(g, tokens, 2, d, dtype=F32)
+    pos = torch.randint(-2**31, 2**31 - 1, (tokens,), generator=g, device="cuda").to(torch.int32)
+    pos[:8] = ints([0, 1, -1, 2**20, 2**24 + 1, 2**30, 2**31 - 1, -2**31])
+    out = isa.spin_rope(lt, x, pos, out=torch.full_like(x, math.nan))
+    with decimal.localcontext(prec=60):
+        two_pi = 2 * decimal.Decimal("3.14159265358979323846264338327950288419716939937510582097494")
+        f = [decimal.Decimal(base) ** (decimal.Decimal(-2 * i) / d) / decimal.Decimal(factor) for i in range(d // 2)]
+        angle = torch.tensor([[float(p * fi % two_pi) for fi in f] for p in pos.tolist()], dtype=torch.float64,
+                             device="cuda")[:, None]
+    a, b = x[..., 0::2].double(), x[..., 1::2].double()
+    want = torch.stack([a * angle.cos() - b * angle.sin(), a * angle.sin() + b * angle.cos()], dim=-1).flatten(-2)
+    # radians: the fraction's cut (2^-32 of a turn) and float, f's rounding (a double's half step from each of pow and
+    # the division); of cos and sin: sincospif's step, 2^-24; each product and the sum half a step of |a| + |b|
+    err = 2 * math.pi * (2.0 ** -26 + 2.0 ** -32) + pos.double().abs()[:, None, None] * torch.tensor(
+        [float(fi) for fi in f], dtype=torch.float64, device="cuda") * 2.0 ** -52 + 3 * 2.0 ** -24
+    bound = ((a.abs() + b.abs()) * err).repeat_interleave(2, dim=-1)
+    ref.check(out, want, bound)
 
 
 def test_rope_of_no_tokens():
