@@ -179,13 +179,30 @@ def _cache(lt: SpinLatent, cache: torch.Tensor, block_table: torch.Tensor):
             _dense(lt, block_table, "block_table", torch.int32, (lt.requests, columns)), columns)
 
 
-def _overlap(a: torch.Tensor, b: torch.Tensor) -> bool:
-    """Whether the byte ranges of two tensors meet."""
+def _steps(*dims):
+    """(stride, size) of those of the dimensions that have more than one place, the smallest stride first."""
+    return sorted(d for d in dims if d[1] > 1)
+
+
+def _overlap(a: torch.Tensor, b: torch.Tensor, dims: Optional[tuple]) -> bool:
+    """Whether two tensors [.., .., width] of one shape share an element.
+    ``dims``: (stride, size) of the outer dimensions, where both tensors have
+    these strides and their rows do not overlap; None: the answer is whether
+    the byte ranges meet."""
     def span(t):
         last = sum((n - 1) * s for n, s in zip(t.shape, t.stride()))
         return t.data_ptr(), t.data_ptr() + (last + 1) * t.element_size()
     (a0, a1), (b0, b1) = span(a), span(b)
-    return a.numel() > 0 and b.numel() > 0 and a0 < b1 and b0 < a1
+    if a.numel() == 0 or a0 >= b1 or b0 >= a1:
+        return False
+    if dims is None or (b0 - a0) % a.element_size():
+        return True
+    # a row of a against one of b, n places of a dimension apart: as all rows behind a dimension fit its stride, only
+    # the two n whose rows are nearest can meet
+    apart = [(b0 - a0) // a.element_size()]
+    for step, size in reversed(_steps(*dims)):
+        apart = [d - n * step for d in apart for n in (d // step, d // step + 1) if abs(n) < size]
+    return any(abs(d) < a.shape[-1] for d in apart)
 
 
 # --------------------------------------------------------------------------
@@ -201,7 +218,8 @@ def spin_rope(lt: SpinLatent, x: torch.Tensor, positions: torch.Tensor, offset: 
               out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """Rotates elements offset .. offset + rope_dim - 1 of every head of x
     [tokens, heads, head_dim] by its token's position; ``out`` None: in place.
-    Returns the tensor it wrote."""
+    Where the memory of out lies among that of x (parts of one packed tensor),
+    they have the same strides.  Returns the tensor it wrote."""
     out = x if out is None else out
     shape = x.shape
     if len(shape) != 3 or out.shape != shape:
@@ -222,13 +240,13 @@ def spin_rope(lt: SpinLatent, x: torch.Tensor, positions: torch.Tensor, offset: 
         raise ValueError("the last dimension of x and out must be contiguous")
     # heads of out one behind the other, in either order of tokens and heads
     if not (oh >= width and ot >= oh * (heads - 1) + width):
-        steps = sorted((n_s[1], n_s[0]) for n_s in ((tokens, ot), (heads, oh)) if n_s[0] > 1)
         reach = width
-        for step, n in steps:
+        for step, n in _steps((ot, tokens), (oh, heads)):
             if step < reach:
                 raise ValueError("the heads of out must not overlap")
             reach += step * (n - 1)
-    if out is not x and (out.data_ptr() != x.data_ptr() or ot != xt or oh != xh) and _overlap(x, out):
+    if out is not x and (out.data_ptr() != x.data_ptr() or ot != xt or oh != xh) and _overlap(
+            x, out, ((ot, tokens), (oh, heads)) if ot == xt and oh == xh else None):
         raise ValueError("out must be x or not overlap it")
     _call("spin_rope", lt.handle, tokens, heads, width, offset, x.data_ptr(), xt, xh,
           _dense(lt, positions, "positions", torch.int32, (tokens,)), out.data_ptr(), ot, oh, _stream(lt, stream))

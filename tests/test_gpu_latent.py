@@ -155,6 +155,21 @@ def test_rope_angles_at_any_position(base, scaling, factor):
     ref.check(out, want, bound)
 
 
+@pytest.mark.parametrize("dtype,half", [(BF16, False), (F32, True)])
+def test_rope_into_the_other_part_of_a_packed_tensor(dtype, half):
+    lt = handle(1, 64, bf16=dtype == BF16, rope_layout=int(half))
+    g = gen(8)
+    x = randn(g, 70, 3, 192, dtype=dtype)
+    pos = torch.randint(0, 100000, (70,), generator=g, device="cuda").to(torch.int32)
+    want = isa.spin_rope(lt, x, pos, offset=128, out=torch.empty_like(x))
+    for pad in (0, 1):  # in 16-byte pieces, and not
+        room = torch.full((70, 3, 384 + pad), math.nan, dtype=dtype, device="cuda")
+        for a, b in ((0, 192), (192 + pad, 0)):
+            room[..., a:a + 192] = x
+            isa.spin_rope(lt, room[..., a:a + 192], pos, offset=128, out=room[..., b:b + 192])
+            assert torch.equal(room[..., b:b + 192], want) and torch.equal(room[..., a:a + 192], x)
+
+
 def test_rope_of_no_tokens():
     lt = handle(1, 64)
     x = torch.empty((0, 4, 64), dtype=BF16, device="cuda")

@@ -4,6 +4,7 @@ launched), and the binding's shape, stride and overlap checks.  No call here
 touches a GPU: where a handle is needed, the binding's checks run against one
 that was never created, and they refuse before the library is reached."""
 import ctypes
+import itertools
 
 import pytest
 import torch
@@ -152,6 +153,40 @@ def test_rope_refuses_wrong_tensors(lib):
     big = torch.zeros(5 * 4 * 128 + 64, dtype=torch.bfloat16)
     with pytest.raises(ValueError, match="overlap"):
         isa.spin_rope(lt, big[:-64].view(5, 4, 128), pos, out=big[64:].view(5, 4, 128))
+
+
+@pytest.mark.parametrize("shape,strides", [((5, 4, 8), (64, 16, 1)), ((5, 4, 8), (40, 8, 1)), ((3, 4, 8), (10, 50, 1)),
+                                           ((1, 6, 8), (0, 19, 1)), ((6, 1, 8), (19, 0, 1)), ((1, 1, 8), (0, 0, 1)),
+                                           ((4, 3, 8), (33, 11, 1))])
+def test_overlap_of_views_with_the_same_strides(shape, strides):
+    """Every distance of two views against the sets of their elements."""
+    room = torch.zeros(2000, dtype=torch.bfloat16)
+    at = lambda first: torch.as_strided(room, shape, strides, first)
+    cells = lambda first: {first + sum(i * s for i, s in zip(place, strides))
+                           for place in itertools.product(*map(range, shape))}
+    dims = tuple(zip(strides[:2], shape[:2]))
+    for distance in range(-500, 500):
+        meet = bool(cells(700) & cells(700 + distance))
+        assert latent._overlap(at(700), at(700 + distance), dims) == meet, distance
+        assert latent._overlap(at(700), at(700 + distance), None) >= meet
+
+
+def test_rope_takes_parts_of_one_packed_tensor(lib, monkeypatch):
+    """Queries and their rotated copies side by side, per head and per token; the same a step closer overlap."""
+    lt = _NoHandle(_cfg())
+    monkeypatch.setattr(latent, "_stream", lambda lt, stream: None)
+    pos = torch.zeros(5, dtype=torch.int32)
+    room = torch.zeros((5, 4, 256), dtype=torch.bfloat16)
+    by_token = torch.zeros((5, 8, 128), dtype=torch.bfloat16)
+    for x, out in ((room[..., :128], room[..., 128:]), (room[..., 128:], room[..., :128]),
+                   (by_token[:, :4], by_token[:, 4:]), (room[..., :64], room[..., 64:128])):
+        with pytest.raises(isa.SpinError) as e:  # past the checks: the library has no handle
+            isa.spin_rope(lt, x, pos, out=out)
+        assert e.value.status == 4
+    for x, out in ((room[..., :128], room[..., 120:248]), (by_token[:, :5], by_token[:, 3:]),
+                   (room[..., :128], room.view(5, 8, 128)[:, 1:5])):
+        with pytest.raises(ValueError, match="overlap"):
+            isa.spin_rope(lt, x, pos, out=out)
 
 
 def test_prefill_without_slots_is_refused(lib):
