@@ -531,7 +531,9 @@ SPIN_API spin_status spin_rope(spin_latent lt, int64_t tokens, int heads, int he
  * request with ctx_len < 1, a row_count outside 0..rows or a last slot past
  * max_slots sets ERR_CTX_LEN (bit 0) or ERR_ACCEPTED (bit 2) and writes
  * nothing (with row_count 0 its ctx_len is not looked at); a page outside the
- * cache sets ERR_PAGE (bit 1) and that token is not written.  Two rows that share a slot of one page leave either's entry. */
+ * cache sets ERR_PAGE (bit 1) and that token is not written.  No two tokens of
+ * a call may go to one slot of one page (requests that share the page they
+ * write to): its entry could then hold parts of both. */
 SPIN_API spin_status spin_latent_append(spin_latent lt, int rows, const void* c_dev, int64_t c_token_stride,
                                         const void* kr_dev, int64_t kr_token_stride, void* cache, int32_t num_pages,
                                         const int32_t* block_table, int32_t bt_stride, const int32_t* ctx_len_dev,
