@@ -548,6 +548,8 @@ SPIN_API spin_status spin_latent_append(spin_latent lt, int rows, const void* c_
  *   0..p_r;
  *   out [Q][rows][num_heads][latent_dim] in dtype, lse [Q][rows][num_heads]
  *   fp32 (NULL: not written): the natural logarithm of the sum of exp(s_j).
+ * The weights are rounded to dtype where they meet the entries, or not at all;
+ * their sums are of the unrounded ones, in fp32.
  * A row that attends to nothing gets out = 0 and lse = -inf, as does a
  * request whose ctx_len is out of range (ERR_CTX_LEN).  A slot whose page
  * lies outside the cache sets ERR_PAGE and is skipped.  Entries that a row
@@ -568,8 +570,8 @@ SPIN_API spin_status spin_latent_attention(spin_latent lt, int rows, const void*
  *   w_kv [num_heads][nope_dim + v_dim][latent_dim] contiguous: W_uk then W_uv
  *   of each head;
  *   out [Q][rows][num_heads][v_dim]; rows >= row_count are left as they are.
- * Expanded keys and values, and the weights that meet the values, are rounded
- * to dtype.  A request whose lengths are out of range sets ERR_CTX_LEN or
+ * Expanded keys and values are rounded to dtype, the weights where they meet the
+ * values to dtype or not at all.  A request whose lengths are out of range sets ERR_CTX_LEN or
  * ERR_ACCEPTED, one that no longer fits prefill_slots (in request order)
  * ERR_CAPACITY (bit 4), one with a page outside the cache among those of its
  * slots ERR_PAGE; its rows stay unwritten.  Slots that a row does not see never
