@@ -570,16 +570,16 @@ SPIN_API spin_status spin_latent_attention(spin_latent lt, int rows, const void*
  *   w_kv [num_heads][nope_dim + v_dim][latent_dim] contiguous: W_uk then W_uv
  *   of each head;
  *   out [Q][rows][num_heads][v_dim]; rows >= row_count are left as they are.
- * Expanded keys and values are rounded to dtype, the weights where they meet the
- * values to dtype or not at all.  A request whose lengths are out of range sets ERR_CTX_LEN or
- * ERR_ACCEPTED, one that no longer fits prefill_slots (in request order)
- * ERR_CAPACITY (bit 4), one with a page outside the cache among those of its
- * slots ERR_PAGE; its rows stay unwritten.  Slots that a row does not see never
- * reach its result, whatever latents they hold.  Where an expanded value is not
- * finite in dtype (by its latent, or past dtype's range), rows that see its slot
- * are not finite in that element of the head, and may be NaN in all of them.
- * SPIN_EUNSUPPORTED without prefill_slots, or where num_requests * num_heads *
- * ceil(rows / 256) is near 2^31 or more. */
+ * Expanded keys and values are rounded to dtype, the weights where they meet
+ * the values to dtype or not at all.  A request whose lengths are out of range
+ * sets ERR_CTX_LEN or ERR_ACCEPTED, one that no longer fits prefill_slots (in
+ * request order) ERR_CAPACITY (bit 4), one with a page outside the cache among
+ * those of its slots ERR_PAGE; its rows stay unwritten.  Slots that a row does
+ * not see never reach its result, whatever latents they hold.  Where an expanded
+ * value is not finite in dtype (by its latent, or past dtype's range), rows that
+ * see its slot are not finite in that element of the head, and may be NaN in
+ * all of them.  SPIN_EUNSUPPORTED without prefill_slots, or where num_requests *
+ * num_heads * ceil(rows / 256) is near 2^31 or more. */
 SPIN_API spin_status spin_latent_prefill(spin_latent lt, int rows, const void* cache, int32_t num_pages,
                                          const int32_t* block_table, int32_t bt_stride, const void* q,
                                          int64_t q_token_stride, int64_t q_head_stride, const void* w_kv,

@@ -5,10 +5,10 @@
 //               matrix product M = slots, N = 128 twice, K = 512.  A block keeps
 //               the latents of 128 slots in TMEM and streams the heads' weights,
 //               160 KB in flight, so L2 -> SM carries 256 KB a unit (slot tile,
-//               head) instead of 384.  105 us for 16K slots x 32 heads, 1.30
+//               head) instead of 384.  109 us for 16K slots x 32 heads, 1.26
 //               PFLOP/s, where a large plain product reaches 1.65: a unit
-//               takes 4780 cycles, its products alone 4160, bringing in a slot
-//               tile 6000.
+//               takes some 4800 cycles, its products alone 4160, bringing in a
+//               slot tile 6000.
 // k_prefill_tc  causal attention of 256 rows of one head: two 128-row tiles take
 //               turns on the tensor cores, one's softmax under the other's
 //               products:
@@ -19,10 +19,10 @@
 //               reference moves only where a row's maximum has grown by more
 //               than 8 (log2 units), and then its warp rescales O.  K and V come
 //               in 16 KB blocks (K: 64 columns of the 128 keys, V: 64 keys)
-//               through one ring of eight, in the order of use.  926 us for 4096
-//               rows at the end of 16K slots x 32 heads, alone on a cool card
-//               (1.30 PFLOP/s); in a steady run the power limit takes a tenth of
-//               the clock.  Bound by the products, which read 128 bytes of shared
+//               through one ring of eight, in the order of use.  For 4096 rows
+//               at the end of 16K slots x 32 heads some 940 us (1.28 PFLOP/s) of
+//               the call's 1067, on a cool card; in a steady run the power limit
+//               takes a tenth of the clock.  Bound by the products, which read 128 bytes of shared
 //               memory a cycle in S (all there is), together with the chain S ->
 //               weights -> second product -> S of each row tile: P takes the place
 //               of its S, and TMEM has no room for another.  Without the softmax
@@ -38,7 +38,7 @@
 // not see or hardly weighs: its own values and weights then fall below fp16's
 // smallest where such a slot is some 2^14 times larger.
 //
-// The CUDA-core kernels of the same steps took 260 ms where these take 1.05.
+// The CUDA-core kernels of the same steps took 260 ms where these take 1.07.
 #include <algorithm>
 
 #include "latent_internal.cuh"
