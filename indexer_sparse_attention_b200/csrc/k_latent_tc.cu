@@ -484,7 +484,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       w.open(a);
       if (threadIdx.x == 0 && w.t0 == 0 && attn_end(a, w.q, w.r) == 0)
         raise_error(a.err, ERR_CTX_LEN, w.q, (uint32_t)a.ctx_len[w.q]);
-      float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+      float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;  // references (scores) and sums
+      float r0 = 0.f, r1 = 0.f, far0 = 0.f, far1 = 0.f;  // references times the factor, or (far ones) as they are
       int flags;
       bool alive = true;
       do {
@@ -521,17 +522,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           bool grow = flags & 1;  // (the first tile: there is no reference yet)
           d0 = d1 = 0.f;
           if (ok && mine && (pass || !(flags & 1))) {
-            const float r0 = m0 == -INFINITY ? 0.f : m0, r1 = m1 == -INFINITY ? 0.f : m1;
             float x0 = -INFINITY, x1 = -INFINITY;
 #pragma unroll
             for (int n = 0; n < 4; ++n) {
-              const float s0 = fmaf(__uint_as_float(s[4 * n]), a.scale_log2, -r0);
-              const float s1 = fmaf(__uint_as_float(s[4 * n + 1]), a.scale_log2, -r0);
-              const float s2 = fmaf(__uint_as_float(s[4 * n + 2]), a.scale_log2, -r1);
-              const float s3 = fmaf(__uint_as_float(s[4 * n + 3]), a.scale_log2, -r1);
-              x0 = fmaxf(x0, fmaxf(s0, s1));
-              x1 = fmaxf(x1, fmaxf(s2, s3));
-              const float p0 = ex2(s0), p1 = ex2(s1), p2 = ex2(s2), p3 = ex2(s3);
+              float x[4];  // two tokens of each head: (score - far) * scale - r
+              sub2(x[0], x[1], __uint_as_float(s[4 * n]), __uint_as_float(s[4 * n + 1]), far0);
+              sub2(x[2], x[3], __uint_as_float(s[4 * n + 2]), __uint_as_float(s[4 * n + 3]), far1);
+              fma2(x[0], x[1], x[0], x[1], a.scale_log2, -r0);
+              fma2(x[2], x[3], x[2], x[3], a.scale_log2, -r1);
+              x0 = fmaxf(x0, fmaxf(x[0], x[1]));
+              x1 = fmaxf(x1, fmaxf(x[2], x[3]));
+              const float p0 = ex2(x[0]), p1 = ex2(x[1]), p2 = ex2(x[2]), p3 = ex2(x[3]);
               d0 += p0 + p1;
               d1 += p2 + p3;
               p[2 * n] = pack_bf16(p0, p1);
@@ -560,13 +561,25 @@ __global__ void __launch_bounds__(kThreads, 1)
           alive = !bar_or(1, kSoft, !ok);
           if (!alive) break;
           if (mine) {
-            const float n0 = fmaxf(m0, fmaxf(t0, halves[half ^ 1][hA]) * a.scale_log2);
-            const float n1 = fmaxf(m1, fmaxf(t1, halves[half ^ 1][hA + 8]) * a.scale_log2);
-            const float f0 = n0 == -INFINITY ? 1.f : ex2(m0 - n0), f1 = n1 == -INFINITY ? 1.f : ex2(m1 - n1);
+            const float n0 = fmaxf(m0, fmaxf(t0, halves[half ^ 1][hA]));
+            const float n1 = fmaxf(m1, fmaxf(t1, halves[half ^ 1][hA + 8]));
+            const float f0 = n0 == -INFINITY ? 1.f : moved(m0, n0, a.scale_log2);
+            const float f1 = n1 == -INFINITY ? 1.f : moved(m1, n1, a.scale_log2);
             l0 *= f0;
             l1 *= f1;
             m0 = n0;
             m1 = n1;
+            r0 = m0 == -INFINITY ? 0.f : m0 * a.scale_log2;
+            r1 = m1 == -INFINITY ? 0.f : m1 * a.scale_log2;
+            far0 = far1 = 0.f;
+            if (fabsf(r0) >= kFar) {
+              far0 = m0;
+              r0 = 0.f;
+            }
+            if (fabsf(r1) >= kFar) {
+              far1 = m1;
+              r1 = 0.f;
+            }
             if (half == 0 && (lane & 3) == 0) {
               ms.fac[hA] = f0;
               ms.fac[hA + 8] = f1;
@@ -632,7 +645,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const int h = hA + 8 * i;
-          const float m = i ? m1 : m0, l = (i ? l1 : l0) + halves[1][h];
+          const float m = (i ? m1 : m0) * a.scale_log2, l = (i ? l1 : l0) + halves[1][h];
           if (whole) {
             ms.fac[h] = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
             if (a.lse && h0 + h < H)

@@ -809,7 +809,10 @@ __global__ void __launch_bounds__(kAttThreads, 1)
     const int pos = pos0 + t * kRowTile + tid - i0 * kRowTile;  // this thread's row, from the part's first key
     const int whole = (pos0 + t * kRowTile + 1) / 64 - 2 * i0;  // halves that every row of the tile sees whole
     const float scale = a.scale_log2;
-    float m = -INFINITY, l = 0.f;
+    const float lazy = kLazy / scale;  // (infinite where no score can grow so far)
+    float M = -INFINITY, l = 0.f;      // the reference, a score
+    float limit = -INFINITY, ref = 0.f;  // the score that moves it, and M * scale (0 where M is far or nothing is seen)
+    bool far = false, any_far = false;  // this row's M is far, one of the warp's rows'
     bool ok = true;
     // The first slot whose values are not finite (they are stored as zeros): a row that sees it becomes NaN.
     const int32_t* odd = a.odd + h * (a.cap / kSlotTile) + off / kSlotTile + i0;
@@ -838,14 +841,20 @@ __global__ void __launch_bounds__(kAttThreads, 1)
 #pragma unroll
         for (int k = 0; k < 4; ++k)
           mt[k] = max3(mt[k], __uint_as_float(s[0][c + k]), __uint_as_float(s[1][c + k]));
-      const float top = fmaxf(fmaxf(mt[0], mt[1]), fmaxf(mt[2], mt[3])) * scale;
-      // (at the first half m is -inf; a row's reference moves by its own maximum alone, so that its bits do not
+      const float top = fmaxf(fmaxf(mt[0], mt[1]), fmaxf(mt[2], mt[3]));
+      // (at the first half M is -inf; a row's reference moves by its own maximum alone, so that its bits do not
       // depend on what its warp's other rows see)
-      const bool grown = top > m + kLazy;
+      const bool grown = top > limit;
       if (__any_sync(0xffffffffu, grown)) {
-        const float mn = grown ? top : m;
-        const float f = grown ? ex2(m - mn) : 1.f;
-        m = mn;
+        const float f = grown ? moved(M, top, scale) : 1.f;
+        if (grown) {
+          M = top;
+          limit = M + lazy;
+          ref = M * scale;
+          far = fabsf(ref) >= kFar;
+          if (far) ref = 0.f;
+        }
+        any_far = __any_sync(0xffffffffu, far);
         l *= f;
         if (j > 0) {
           // (of the second products only the last can still be running: S, or the half before, waited for the others)
@@ -863,7 +872,23 @@ __global__ void __launch_bounds__(kAttThreads, 1)
           }
         }
       }
-      const float ref = m == -INFINITY ? 0.f : m;
+      if (any_far) {
+        // the scores less M, by way of their place in TMEM (64 subtractions here would cost every row)
+#pragma unroll 1
+        for (int c = 0; c < 64; c += 16) {
+          uint32_t x[16];
+          tmem_ld16(at + c, x);
+          tmem_wait_ld();
+#pragma unroll
+          for (int k = 0; k < 16; ++k)
+            x[k] = c + k > pos - j * 64 ? 0xff800000u : __float_as_uint(__uint_as_float(x[k]) - (far ? M : 0.f));
+          tmem_st16(at + c, x);
+        }
+        tmem_wait_st();
+        tmem_ld32(at, s[0]);
+        tmem_ld32(at + 32, s[1]);
+        tmem_wait_ld();
+      }
       float sum[4] = {0.f, 0.f, 0.f, 0.f};
       uint32_t p[32];
 #pragma unroll
@@ -896,7 +921,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
     if (ok && w.parts > 1) {
       // a part: unnormalised, for the join
       const int64_t at = (int64_t)w.slot * 2 * kRowTile + t * kRowTile + tid;
-      if (tid < rows) a.part_ml[at] = make_float2(m, l);
+      if (tid < rows) a.part_ml[at] = make_float2(M * scale, l);
       if (nt) {
         fence_after();
 #pragma unroll 1

@@ -265,6 +265,13 @@ __device__ __forceinline__ void add2(float& d0, float& d1, float a0, float a1) {
       : "+f"(d0), "+f"(d1)
       : "f"(a0), "f"(a1));
 }
+// (d0, d1) = (a0, a1) - c.
+__device__ __forceinline__ void sub2(float& d0, float& d1, float a0, float a1, float c) {
+  asm("{\n\t.reg .b64 a, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 c, {%4, %4};\n\t"
+      "add.rn.f32x2 d, a, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d0), "=f"(d1)
+      : "f"(a0), "f"(a1), "f"(-c));
+}
 
 // The largest of three.
 __device__ __forceinline__ float max3(float a, float b, float c) {
@@ -278,6 +285,17 @@ __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+// Softmax weights are 2^(s c - m) for scores s, a factor c and a reference m =
+// M c, M a score: one multiply-add each, of the rounded m.  Its rounding is the
+// same factor on all weights, 2^r with |r| <= 2^-25 |m|, and nothing to them or
+// their sum until r is of a float's exponents' size.  From kFar on the
+// difference is taken of the scores themselves, (s - M) c.
+constexpr float kFar = 67108864.f;  // 2^26: r up to 2
+// What a reference's move from M (-inf: none yet) to a greater N makes of the weights and sums so far.
+__device__ __forceinline__ float moved(float M, float N, float c) {
+  const float m = M * c, n = N * c;
+  return ex2(fmaxf(fabsf(m), fabsf(n)) < kFar ? m - n : (M - N) * c);
 }
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);

@@ -445,6 +445,44 @@ def test_attention_large_logits_and_one_sided_weights():
     check_attention(lt, 1, cache, bt, ql, qr, ctx, None, out, lse)
 
 
+def ranked_keys(kr, order, power, sign):
+    """Rotary parts of tokens whose logits are (rank - 0 or n) 2^power (exact in fp32): the query's first two elements
+    are 2^(power + 4) and 2^power."""
+    rank = order - (order.numel() if sign < 0 else 0)
+    kr.zero_()
+    kr[:, 0], kr[:, 1] = torch.div(rank, 16, rounding_mode="floor"), rank % 16
+
+
+@pytest.mark.parametrize("dtype,H", [(BF16, 16), (BF16, 128), (F32, 8)])
+@pytest.mark.parametrize("power", [20, 24, 31, 40, 60, 110])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_attention_logits_of_any_size(power, sign, dtype, H):
+    """All weight on the token of the largest logit, wherever it lies: the output is its latent up to roundings."""
+    lt, cache, bt, ql, qr, ctx, topk = attention_case(3, 2, H, 300, [900, 65, 400], 64, dtype, 512, 64)
+    ql.zero_()
+    qr.zero_()
+    qr[..., 0], qr[..., 1] = 2.0 ** (power + 4), 2.0 ** power
+    g = gen(power)
+    for t in (topk, None):
+        for _ in range(4):
+            want, want_lse = torch.empty((3, 2, H, 512), dtype=dtype, device="cuda"), torch.empty((3, 2, H), device="cuda")
+            for q, c in enumerate(ctx.tolist()):
+                order = torch.randperm(c + 1, generator=g, device="cuda")
+                kv = randn(g, c + 1, 576, dtype=dtype)
+                ranked_keys(kv[:, 512:], order, power, sign)
+                put(cache, bt, q, torch.arange(c + 1, device="cuda"), kv)
+                for r in range(2):
+                    s = attended(t, q, r, c + r)
+                    best = s[order[s].argmax()]
+                    want[q, r] = kv[best, :512]
+                    want_lse[q, r] = float(order[best] - (c + 1 if sign < 0 else 0)) * 2.0 ** power * lt.cfg.softmax_scale
+            out, lse = run_attention(lt, 2, cache, bt, ql, qr, ctx, t)
+            # the weight, near 1, in bf16 and the output: half a step each
+            ref.check(out, want.double(), 2.1 * ref.half_step(dtype) * want.double().abs())
+            # the scale by log2 e and back: three roundings of 2^-24
+            assert ((lse.double() - want_lse.double()).abs() <= 4 * 2.0 ** -24 * want_lse.double().abs()).all()
+
+
 def test_attention_passes_nan_of_an_attended_token_to_its_row_alone():
     lt, cache, bt, ql, qr, ctx, topk = attention_case(2, 2, 16, 64, [300, 300], 64, BF16, 512, 64)
     out, lse = run_attention(lt, 2, cache, bt, ql, qr, ctx, topk)
@@ -799,6 +837,34 @@ def test_prefill_rows_have_the_same_bits_whatever_comes_behind_them(power, ctx0,
         q2[0, row] *= 2.0 ** power
         got = run_prefill(lt, 200, cache, bt, q2, w, ctx, count)
         assert torch.equal(got[0, :row], out[0, :row]) and torch.equal(got[0, row + 1:], out[0, row + 1:]), row
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("power", [20, 24, 31, 40, 60, 110])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_prefill_logits_of_any_size(power, sign, dtype):
+    """All weight on the visible slot of the largest logit, which changes from row to row (every slot of the chunk is a
+    new largest with a chance that falls with its position): the output is its value."""
+    lt, cache, bt, qv, w, ctx, count = prefill_case(2, 200, 3, [2200, 40], [200, 130], 64, dtype, 512, 64, 128, 128)
+    w[:, :128] = 0
+    qv.zero_()
+    qv[..., 128], qv[..., 129] = 2.0 ** (power + 4), 2.0 ** power
+    g = gen(power)
+    for rising in (False, True):  # (the last rows' slots the largest, in order: the reference moves all the way)
+        want = torch.full((2, 200, 3, 128), 7.0, dtype=torch.float64, device="cuda")
+        for q, (c, n) in enumerate(zip(ctx.tolist(), count.tolist())):
+            end = c - 1 + n
+            slots = torch.arange(end, device="cuda")
+            order = slots if rising else torch.randperm(end, generator=g, device="cuda")
+            kv = randn(g, end, 576, dtype=dtype)
+            ranked_keys(kv[:, 512:], order, power, sign)
+            put(cache, bt, q, slots, kv)
+            best = order.cummax(0).indices[c - 1:]
+            want[q, :n] = torch.einsum("rc,hvc->rhv", kv[best, :512].double(), w[:, 128:].double())
+        out = run_prefill(lt, 200, cache, bt, qv, w, ctx, count)
+        # half a step each of the value, the weight (near 1) and the output, and the value's sum over 512 products, each
+        # a step of 2^-24 of the sum of |c| |w|, below 40 (512 x 0.8 x 0.8 x 512^-1/2 = 14.5 on average)
+        ref.check(out, want, 3.1 * ref.half_step(dtype) * want.abs() + 512 * 2.0 ** -24 * 40)
 
 
 @pytest.mark.parametrize("Q,fit", [(30, 17), (40, 17), (400, 341)])
