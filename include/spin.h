@@ -482,7 +482,7 @@ typedef struct {
   int32_t rope_layout;    /* spin_rope_layout */
   int32_t rope_scaling;   /* spin_rope_scaling */
   int32_t rope_original;  /* SPIN_ROPE_YARN: positions the frequencies were made for, >= 1 */
-  float softmax_scale;    /* scale of the logits, finite and > 0 */
+  float softmax_scale;    /* scale of the logits, > 0, finite in units of log2 too (times log2 e) */
   float beta_fast;        /* SPIN_ROPE_YARN (32), > beta_slow */
   float beta_slow;        /* SPIN_ROPE_YARN (1), > 0 */
   float attn_factor;      /* SPIN_ROPE_YARN: factor on cos and sin, or 0 */

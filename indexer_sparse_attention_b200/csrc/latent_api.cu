@@ -56,6 +56,9 @@ struct DeviceGuard {
 
 bool eights(int x, int hi) { return x >= 8 && x <= hi && x % 8 == 0; }
 
+// The softmax scale in log2 units, which the kernels use.
+float scale_log2(const spin_latent_config* c) { return (float)((double)c->softmax_scale * 1.4426950408889634); }
+
 bool valid_config(const spin_latent_config* c) {
   if (!c) return false;
   if (c->num_requests < 1 || c->num_requests > 16383) return false;  // Q * rows fits a grid's y
@@ -68,7 +71,7 @@ bool valid_config(const spin_latent_config* c) {
   if (c->prefill_slots < 0 || c->prefill_slots % kSlotTile) return false;
   if (c->prefill_slots && (!eights(c->nope_dim, 256) || !eights(c->v_dim, 256))) return false;
   if (c->dtype != SPIN_F32 && c->dtype != SPIN_BF16) return false;
-  if (!(c->softmax_scale > 0.0f) || !std::isfinite(c->softmax_scale)) return false;
+  if (!(c->softmax_scale > 0.0f) || !std::isfinite(scale_log2(c))) return false;
   if (c->rope_layout < SPIN_ROPE_INTERLEAVED || c->rope_layout > SPIN_ROPE_HALF) return false;
   if (c->rope_scaling < SPIN_ROPE_PLAIN || c->rope_scaling > SPIN_ROPE_YARN) return false;
   if (!(c->rope_base > 1.0) || !std::isfinite(c->rope_base)) return false;
@@ -317,7 +320,7 @@ spin_status spin_latent_attention(spin_latent lt, int rows, const void* cache, i
   const int64_t per16 = c.dtype == SPIN_BF16 ? 8 : 4;
   a.q_vec = ((uintptr_t)q_latent & 15) == 0 && ((uintptr_t)q_rope & 15) == 0 && ql_token_stride % per16 == 0 &&
             ql_head_stride % per16 == 0 && qr_token_stride % per16 == 0 && qr_head_stride % per16 == 0;
-  a.scale_log2 = (float)((double)c.softmax_scale * 1.4426950408889634);
+  a.scale_log2 = scale_log2(&c);
   a.out = out;
   a.lse = lse;
   a.err = lt->err;
@@ -409,7 +412,7 @@ spin_status spin_latent_prefill(spin_latent lt, int rows, const void* cache, int
   a.odd = lt->odd;
   a.part = lt->part;
   a.part_ml = lt->part_ml;
-  a.scale_log2 = (float)((double)c.softmax_scale * 1.4426950408889634);
+  a.scale_log2 = scale_log2(&c);
   a.err = lt->err;
   const int bf16 = c.dtype == SPIN_BF16;
   const int64_t per16 = bf16 ? 8 : 4;

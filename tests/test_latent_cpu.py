@@ -61,6 +61,11 @@ def test_invalid_configs_are_refused(lib, over):
                                   ctypes.byref(h)) == 1 and not h.value
 
 
+def test_a_softmax_scale_that_is_infinite_in_log2_units_is_refused(lib):
+    assert isa.spin_latent_bytes(_cfg(softmax_scale=2.3e38)) > 0
+    assert isa.spin_latent_bytes(_cfg(softmax_scale=2.4e38)) == 0
+
+
 def test_a_handle_without_prefill_ignores_its_dims(lib):
     assert isa.spin_latent_bytes(_cfg(prefill_slots=0, nope_dim=0, v_dim=0, softmax_scale=0.1)) > 0
 
