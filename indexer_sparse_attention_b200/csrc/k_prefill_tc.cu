@@ -20,8 +20,8 @@
 //               than 8 (log2 units), and then its warp rescales O.  K and V come
 //               in 16 KB blocks (K: 64 columns of the 128 keys, V: 64 keys)
 //               through one ring of eight, in the order of use.  For 4096 rows
-//               at the end of 16K slots x 32 heads some 940 us (1.28 PFLOP/s) of
-//               the call's 1067, on a cool card; in a steady run the power limit
+//               at the end of 16K slots x 32 heads some 945 us (1.27 PFLOP/s) of
+//               the call's 1075, on a cool card; in a steady run the power limit
 //               takes a tenth of the clock.  Bound by the products, which read 128 bytes of shared
 //               memory a cycle in S (all there is), together with the chain S ->
 //               weights -> second product -> S of each row tile: P takes the place
@@ -38,7 +38,7 @@
 // not see or hardly weighs: its own values and weights then fall below fp16's
 // smallest where such a slot is some 2^14 times larger.
 //
-// The CUDA-core kernels of the same steps took 260 ms where these take 1.07.
+// The CUDA-core kernels of the same steps took 260 ms where these take 1.08.
 #include <algorithm>
 
 #include "latent_internal.cuh"
